@@ -327,6 +327,60 @@ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t byte_in_
   return row * 128u + ((((byte_in_row >> 4) ^ (row & 7u)) << 4) | (byte_in_row & 15u));
 }
 
+// ------------------------------------------------------- warp-level softmax helpers
+// Butterfly reduce-scatter over the 32 lanes of a warp: afterwards lane l holds the
+// reduction of heads [l*N/32, l*N/32 + N/32) in v[0..] (N >= 32), or of head l/2 (N == 16).
+template <int N, bool IS_MAX>
+__device__ __forceinline__ void warp_reduce_scatter(float (&v)[N], int lane) {
+  int n = N;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const bool up = (lane & o) != 0;
+    if (n > 1) {
+      const int half = n >> 1;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i < half) {
+          const float send = up ? v[i] : v[i + half];
+          const float keep = up ? v[i + half] : v[i];
+          const float recv = __shfl_xor_sync(0xffffffffu, send, o);
+          v[i] = IS_MAX ? fmaxf(keep, recv) : keep + recv;
+        }
+      }
+      n = half;
+    } else {
+      const float recv = __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[0] = IS_MAX ? fmaxf(v[0], recv) : v[0] + recv;
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_scattered(float* dst, const float (&v)[N], int lane) {
+  if constexpr (N >= 32) {
+#pragma unroll
+    for (int i = 0; i < N / 32; ++i) dst[lane * (N / 32) + i] = v[i];
+  } else {
+    if ((lane & 1) == 0) dst[lane >> 1] = v[0];
+  }
+}
+
+// 2^x on the special-function unit (relative error about 2^-22, results below 2^-126
+// flushed to zero): the softmax weights are rounded to bf16 right after, so the extra
+// care of exp2f for subnormal results buys nothing.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// TMEM load of HP consecutive columns of this warp's 32 lanes.
+template <int HP>
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float (&v)[HP]) {
+#pragma unroll
+  for (int c = 0; c < HP / 16; ++c) tmem_ld16(taddr + 16 * c, v + 16 * c);
+}
+
 }  // namespace lsa
 
 // ------------------------------------------------------------------- host helpers
