@@ -420,6 +420,141 @@ lsa_status lsa_denoise_labels(const float* logits, int32_t n_windows, int32_t n_
                               int32_t* label_ids, int32_t label_cap, int32_t* label_cnt,
                               int32_t* err, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Paged grouped-query cache: append, one-token attention with score options, eviction.
+ *
+ * Beside the LSA decode path above (one key head, blocks picked by the indexer) the
+ * library serves caches of grouped query heads whose size is bounded by eviction: each
+ * page carries a running score, the attention weight it received, and the pages with the
+ * smallest scores are given back when a sequence holds more than its budget. With
+ * Hkv = 1 the pool is the pool of lsa_decode_attn, and a block table of lsa_gather can be
+ * attended with the options below.
+ *
+ * Sequence b holds the entries j < n_entries[b] of its table row. Entry j is page
+ * block_table[b][j] of the pool and block block_pos[b][j] of the sequence: slot t of it is
+ * position 64 * block_pos[b][j] + t. All pages are full except the last, which holds
+ * tail_len[b] tokens (1..64). The newest token sits at position
+ * x_b = 64 * block_pos[b][n-1] + tail_len[b] - 1.
+ *
+ * The structs are plain data; every pointer is owned by the caller, and the calls read
+ * the structs only while they run. Calls on the same tables must be ordered on the GPU
+ * (one stream, or events); calls that share a workspace must not overlap.
+ */
+#define LSA_DTYPE_BF16 0
+#define LSA_DTYPE_F16  1
+
+typedef struct lsa_paged_tables {
+  int32_t* block_table;  /* device i32 [B][bt_stride] */
+  int32_t* block_pos;    /* device i32 [B][bt_stride], strictly ascending within a sequence's
+                            entries, each in [0, 2^25); NULL: entry j is block j */
+  float* score;          /* device f32 [B][bt_stride]; NULL: no scores are kept */
+  int32_t* n_entries;    /* device i32 [B], 0 .. bt_stride */
+  int32_t* tail_len;     /* device i32 [B], 1 .. 64 (not read where n_entries is 0) */
+  int32_t* free_list;    /* device i32 [B][free_stride]: a stack of free pages per sequence */
+  int32_t* free_cnt;     /* device i32 [B]: pages on the stack, 0 .. free_stride */
+} lsa_paged_tables;
+
+typedef struct lsa_paged_cache {
+  int32_t B;             /* sequences, 1 .. 65536 */
+  int32_t H, Hkv;        /* query heads and key heads; H / Hkv query heads share a key head */
+  int32_t d;             /* head dimension: 128, 256, 384 or 512 */
+  int32_t dtype;         /* LSA_DTYPE_*: type of the pool, of q, k_new, v_new and out */
+  int32_t bt_stride, free_stride;
+  int32_t window;        /* > 0: sliding window in tokens, the newest one included; 0: none */
+  float scale;           /* attention scale, > 0 */
+  float cap;             /* > 0: scores are cap * tanh(scale * q.k / cap); 0: no cap */
+  float decay;           /* factor of a page's score before the new weight is added, 0 .. 1 */
+  uint16_t* pool;        /* device [n_pages][2][Hkv][64][d]: K rows then V rows of each head */
+  int64_t n_pages;       /* n_pages * Hkv <= 2^23 */
+  lsa_paged_tables t;
+  const float* slopes;        /* nullable device f32 [H]: the bias -slopes[h] * (x_b - x) */
+  const int32_t* prefix_len;  /* nullable device i32 [B]: positions below it are always seen */
+  const int32_t* doc_start;   /* nullable device i32 [B]: positions below it are not seen,
+                                 unless they lie in the prefix */
+  void* ws;              /* device workspace of lsa_paged_attn, 16-byte aligned; it needs no
+                            clearing and carries nothing from one call to the next */
+  size_t ws_bytes;
+  int32_t* err;          /* device i32 error word */
+} lsa_paged_cache;
+
+/* sizeof(lsa_paged_cache), for bindings that mirror the struct. */
+size_t lsa_paged_cache_size(void);
+/* Host-side validation of a cache (no device work). */
+lsa_status lsa_paged_check(const lsa_paged_cache* c);
+
+/* lsa_paged_attn -- one new token of every sequence attends over its pages:
+ *
+ *   z_h(x)  = scale * q[b][h] . K(x),   or cap * tanh(that / cap)      (head h reads key
+ *   z_h(x) -= slopes[h] * (x_b - x)                                     head h / (H/Hkv))
+ *   w_h     = softmax of z_h over the positions that are seen:
+ *             x < prefix_len[b]  or  x >= max(doc_start[b], x_b - window + 1)
+ *   out[b][h] = sum_x w_h(x) V(x)
+ *   score[b][j] = decay * score[b][j] + sum_h sum_(x in entry j) w_h(x),  j < n_entries[b]
+ *
+ * A sequence that sees nothing (n_entries 0, or all its positions masked) gets zeros.
+ * Positions that are not seen have no influence whatever their keys and values hold,
+ * infinities and NaN included, and blocks without a seen position are not read. The new
+ * token's own key and value must be in the cache (lsa_paged_append).
+ *
+ *   q    device [B][H][d], 16-byte aligned
+ *   out  device [B][H][d], 16-byte aligned
+ *   c->ws  lsa_paged_attn_workspace_size bytes, where with_score says whether t.score is
+ *          kept and n_sm is the multiprocessor count of the current device
+ * Supported: 1 <= H / Hkv <= 64, H <= 1024. A table entry outside [0, n_pages) sets
+ * LSA_DEVERR_BAD_PAGE and its positions are not seen; a sequence whose n_entries or
+ * tail_len is out of range sets LSA_DEVERR_BAD_SIZE, gets zeros and keeps its scores.
+ * Results do not depend on the order in which thread blocks run. Two launches: the
+ * split attention, then the joining of its parts (a programmatic dependent launch).
+ */
+lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q, uint16_t* out, void* stream);
+size_t lsa_paged_attn_workspace_size(int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                     int32_t bt_stride, int32_t with_score, int32_t n_sm);
+
+/* lsa_paged_append -- put new tokens behind each sequence's last one.
+ *
+ *   k_new, v_new  device [n_tokens][Hkv][d], 16-byte aligned
+ *   tok_off       nullable device i32 [B+1], ascending from >= 0 to <= n_tokens: sequence b
+ *                 gets the tokens tok_off[b] .. tok_off[b+1] - 1 (there may be none);
+ *                 NULL: n_tokens == B and every sequence gets one token
+ *   dst           nullable: where the changes go (NULL: into c->t). Each of its arrays is
+ *                 either the one of c->t or does not overlap it, and has its shape.
+ * Token i goes to slot (held + i) % 64 of entry (held + i) / 64, where held counts the
+ * sequence's tokens. A new entry takes the page on top of the sequence's free stack, the
+ * block position behind the last entry's (0 in an empty sequence), and score 0; the
+ * tables' other entries are left as they are. Then n_entries, tail_len and free_cnt are
+ * written (for every sequence). A sequence whose new tokens need more pages than its
+ * stack holds, or more entries than bt_stride, takes none of them, keeps its counts, and
+ * sets LSA_DEVERR_POOL_CAPACITY. A page outside the pool sets LSA_DEVERR_BAD_PAGE and the
+ * token's rows are not written; sizes out of range set LSA_DEVERR_BAD_SIZE, with no effect
+ * on that sequence.
+ */
+lsa_status lsa_paged_append(const lsa_paged_cache* c, const uint16_t* k_new, const uint16_t* v_new,
+                            int64_t n_tokens, const int32_t* tok_off, const lsa_paged_tables* dst,
+                            void* stream);
+
+/* lsa_paged_evict -- bring every sequence down to `budget` entries.
+ *
+ * A sequence with n_entries[b] > budget keeps its first n_sink entries, its last n_recent
+ * ones, and of those between the budget - n_sink - n_recent with the largest scores (equal
+ * scores: the lower index first; NaN ranks below every number). The kept entries stay in
+ * order at the front of the row, with their positions and scores; the pages of the others
+ * are pushed on the free stack in order. Entries behind the kept ones are left as they
+ * were. Other sequences are copied to dst unchanged.
+ *
+ *   budget        1 .. ; n_sink >= 0, n_recent >= 1 (the tail page stays),
+ *                 n_sink + n_recent <= budget
+ *   dst           nullable: where block_table, block_pos, score, n_entries, tail_len, the
+ *                 pushed part of free_list and free_cnt go (NULL: into c->t). Each of its
+ *                 arrays is either the one of c->t or does not overlap it.
+ * A sequence whose free stack cannot take the freed pages is not trimmed and sets
+ * LSA_DEVERR_POOL_CAPACITY; an n_entries or free_cnt out of range sets LSA_DEVERR_BAD_SIZE,
+ * and the sequence's counts go to dst as they are. t.score must not be NULL. With a
+ * window, slopes, prefix_len or doc_start, t.block_pos must not be NULL (the kept blocks'
+ * positions would be lost).
+ */
+lsa_status lsa_paged_evict(const lsa_paged_cache* c, int32_t budget, int32_t n_sink,
+                           int32_t n_recent, const lsa_paged_tables* dst, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

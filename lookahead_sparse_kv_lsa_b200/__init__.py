@@ -18,7 +18,8 @@ __all__ = ["lsa_index", "lsa_index_lowrank", "index_lowrank_workspace_size", "ls
            "lsa_load_window", "gather_delta_workspace_size", "lsa_denoise_labels",
            "DENOISE_MAX_BLOCKS", "lsa_wait_selftest",
            "lsa_pass_setup", "lsa_append", "lsa_decode_step",
-           "index_workspace_size", "decode_attn_workspace_size", "LsaDecoder", "LsaError",
+           "index_workspace_size", "decode_attn_workspace_size", "LsaDecoder", "LsaPagedCache",
+           "LsaPagedTables", "paged_attn_workspace_size", "LsaError",
            "LsaState", "BLOCK", "TAU", "library_path"]
 
 
@@ -245,4 +246,13 @@ def lsa_step(state: LsaState, step: int, h, q, k_new, v_new, out, stream=None) -
     _lib.check("lsa_step", st)
 
 
+def paged_attn_workspace_size(B: int, H: int, Hkv: int, d: int, bt_stride: int,
+                              with_score: bool, n_sm: Optional[int] = None) -> int:
+    if n_sm is None:
+        n_sm = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(_lib.lib().lsa_paged_attn_workspace_size(B, H, Hkv, d, bt_stride, int(with_score),
+                                                        n_sm))
+
+
 from .decoder import LsaDecoder  # noqa: E402
+from .paged import LsaPagedCache, LsaPagedTables  # noqa: E402

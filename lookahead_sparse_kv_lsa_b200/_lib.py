@@ -21,6 +21,8 @@ DEVERR_BAD_SIZE = 8
 DEVERR_TIMEOUT = 16
 DEVERR_NUMERIC = 32
 
+DTYPE_BF16, DTYPE_F16 = 0, 1
+
 BLOCK = 64
 TAU = 64
 
@@ -47,6 +49,24 @@ class LsaState(C.Structure):
         ("kidx_layer_stride", _i64),
         ("kept_ids", _p), ("kept_pages", _p), ("kept_cnt", _p),
         ("gather_ws", _p), ("gather_ws_bytes", _sz),
+    ]
+
+
+class LsaPagedTablesC(C.Structure):
+    """Mirror of `lsa_paged_tables` (lsa.h)."""
+    _fields_ = [("block_table", _p), ("block_pos", _p), ("score", _p), ("n_entries", _p),
+                ("tail_len", _p), ("free_list", _p), ("free_cnt", _p)]
+
+
+class LsaPagedCacheC(C.Structure):
+    """Mirror of `lsa_paged_cache` (lsa.h)."""
+    _fields_ = [
+        ("B", _i32), ("H", _i32), ("Hkv", _i32), ("d", _i32), ("dtype", _i32),
+        ("bt_stride", _i32), ("free_stride", _i32), ("window", _i32),
+        ("scale", C.c_float), ("cap", C.c_float), ("decay", C.c_float),
+        ("pool", _p), ("n_pages", _i64), ("t", LsaPagedTablesC),
+        ("slopes", _p), ("prefix_len", _p), ("doc_start", _p),
+        ("ws", _p), ("ws_bytes", _sz), ("err", _p),
     ]
 
 
@@ -81,6 +101,14 @@ SIGNATURES = {
     "lsa_decode_step": (_i32, [C.POINTER(LsaState), _i64, _p, _p, _p, _p, _p]),
     "lsa_denoise_labels": (_i32, [_p, _i32, _i32, _i32, C.c_double, _i32, _p, _p, _p, _p, _i32,
                                   _p, _p, _p]),
+    "lsa_paged_cache_size": (_sz, []),
+    "lsa_paged_check": (_i32, [C.POINTER(LsaPagedCacheC)]),
+    "lsa_paged_attn": (_i32, [C.POINTER(LsaPagedCacheC), _p, _p, _p]),
+    "lsa_paged_attn_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "lsa_paged_append": (_i32, [C.POINTER(LsaPagedCacheC), _p, _p, _i64, _p,
+                                C.POINTER(LsaPagedTablesC), _p]),
+    "lsa_paged_evict": (_i32, [C.POINTER(LsaPagedCacheC), _i32, _i32, _i32,
+                               C.POINTER(LsaPagedTablesC), _p]),
     "lsa_wait_selftest": (_i32, [_p, C.c_uint32, _i64, _p, _p]),
 }
 

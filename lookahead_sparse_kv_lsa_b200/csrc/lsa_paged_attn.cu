@@ -1,0 +1,1360 @@
+// One-token attention over a paged cache of grouped query heads, with capped scores, a
+// distance bias, prefix / document / window masks, and the pages' attention weights.
+//
+// Per sequence b, query head h of key head g and seen position x:
+//   z = scale q.K(x), capped: c tanh(z / c), minus slope_h (x_b - x);  w = softmax(z);
+//   out = sum w V(x);  score[page of x] += w.
+// All softmax arithmetic is in log2 units (z * log2 e), in fp32. The bias is taken relative
+// to the last seen position instead of x_b: a constant per head, which the softmax drops,
+// and the differences that matter stay small numbers however long the cache is.
+//
+// What bounds it: every key and value is read once, 4 d Hkv bytes a token against
+// 4 H d flops, so H / Hkv flop per byte; on a B200 that is HBM bandwidth for any group of
+// up to 64 heads, as long as the products run on the tensor cores.
+//
+// Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
+// e2 on (document, window); they are cut into 32-token units, the same for each key head.
+// The units of all (sequence, key head) pairs, in order, are divided evenly over the CTAs;
+// each (CTA, pair) piece is a segment that leaves (O, max, sum) in the workspace slot
+// CTA + pair, and the joining kernel, a programmatic dependent launch, merges the slots of
+// a pair. Nothing waits for another CTA and no counter outlives a call, so a workspace
+// carries no state.
+//
+// Within a segment, tiles of up to 128 tokens run newest first (a bias that falls with the
+// distance then sets the running max once), in a pipeline of three roles:
+//   warp 0    reads the page table and issues TMA loads: Q once per segment, K and V tiles
+//             in 16 KB stages of [128 tokens][64 dims] through a ring;
+//   warp 1    tcgen05.mma: S^T[token][head] = K Q^T (M = 128, N = heads padded to 16, 32 or
+//             64), double buffered in TMEM; O^T[dim][head] += V^T P (M = 128 dims, K = 128
+//             tokens), accumulated in TMEM;
+//   warps 2-5 softmax, one token row per thread: the row's scores stay in registers from the
+//             one TMEM load to the rounding of P. A vote (one barrier with reduction) finds
+//             whether any score exceeds its head's running max by more than 2^8; only then is
+//             the tile max formed and O^T rescaled. Each unit's per-head sums (a butterfly
+//             over the warp's 32 rows) feed the denominators and, where scores are kept, go
+//             to the workspace with the max they refer to.
+// P is written token-major ([128 tokens][heads], 16-byte stores) and read by the tensor cores
+// as an MN-major operand, swizzled by its row size.
+//
+// Rows that are not seen get weight 0, and in a tile that has any, the softmax warps clear
+// their rows of V in shared memory before the product reads them: 0 * NaN would be NaN.
+#include "lsa_common.cuh"
+
+#include <math.h>
+
+namespace lsa {
+namespace paged {
+
+constexpr int PAGE = LSA_BLOCK;
+constexpr int UNIT = 32;                  // tokens per work unit: the rows of a softmax warp
+constexpr int TILE = 128;                 // tokens per tile: the MMA M of S^T
+constexpr int STAGE_BYTES = TILE * 128;   // [128 rows][64 dims] 16-bit = 16 KB
+constexpr int NTHREADS = 192;
+constexpr int MAXREC = 16;                // sequences a CTA plans at a time
+constexpr int YRING = 256;                // units whose pool rows the producer has looked up
+constexpr float RESCALE_LOG2 = 8.0f;      // raise the running max only by more than 2^8
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int JOIN_THREADS = 256;
+constexpr int MAX_CTAS = 512;
+
+// One sequence, as the attention CTAs and the joining kernel see it.
+struct Rec {
+  long long base;    // first unit of its first key head in the batch-wide order
+  long long ref;     // last position of its last seen entry (origin of the bias)
+  long long low;     // positions >= low are seen,
+  int pre;           //   and those < pre
+  int b, units;      // units of one key head; 0: nothing seen
+  int n, tail;       // entries, tokens in the last one
+  int e1, e2;        // seen entries: [0, e1) and [e2, n)
+  int masked;        // whether low / pre exclude any position of a seen entry
+};
+
+// What the joining kernel needs of a sequence (workspace, written by CTA 0).
+struct Plan {
+  long long base;
+  int units, n, e1, e2, tail, pad;
+};
+struct Head {
+  long long U;
+  int ctas, pad;
+};
+
+struct Args {
+  const int32_t* block_table;
+  const int32_t* block_pos;
+  const int32_t* n_entries;
+  const int32_t* tail_len;
+  const int32_t* prefix_len;
+  const int32_t* doc_start;
+  const float* slopes;
+  float* score;
+  uint16_t* out;
+  int32_t* err;
+  Head* head;        // workspace
+  Plan* plan;        // [B]
+  float2* part_ml;   // [slot][G] running max (log2 units) and sum
+  float* part_o;     // [slot][G][d]
+  float2* unit_w;    // [B][bt_stride][2][H] unit sums and the max they refer to
+  long long n_pages;
+  int B, H, Hkv, G, d, bt_stride, window, f16, min_units;
+  float scale, cap, decay;
+};
+
+// First entry whose block position is at least `x` (n if none). Positions ascend strictly, so
+// a run of consecutive blocks at either end answers without a search: the bounds' own
+// entries are looked at first. Whatever the table holds, the answer lies in [0, n].
+__device__ __forceinline__ int first_at_least(const int32_t* pos, int n, long long x) {
+  if (n <= 0) return 0;
+  if (pos == nullptr) return static_cast<int>(x <= 0 ? 0 : x < n ? x : n);
+  const long long first = pos[0], last = pos[n - 1];
+  if (x <= first) return 0;
+  if (x > last) return n;
+  long long lo = n - 1 - (last - x), hi = x - first;   // the answer lies in [lo, hi]
+  lo = lo < 0 ? 0 : lo;
+  hi = hi > n - 1 ? n - 1 : hi;
+  if (hi < lo) return static_cast<int>(lo);            // only where positions do not ascend
+  const bool at_lo = pos[lo] >= x;
+  const bool at_hi = hi > 0 && pos[hi - 1] < x;
+  if (at_lo) return static_cast<int>(lo);
+  if (at_hi) return static_cast<int>(hi);
+  while (lo < hi) {
+    const long long mid = (lo + hi) >> 1;
+    if (pos[mid] >= x) hi = mid; else lo = mid + 1;
+  }
+  return static_cast<int>(lo);
+}
+
+__device__ __forceinline__ bool malformed(const Args& a, int b) {
+  const int n = a.n_entries[b];
+  if (n == 0) return false;
+  const int t = a.tail_len[b];
+  return n < 0 || n > a.bt_stride || t < 1 || t > PAGE;
+}
+
+__device__ __forceinline__ Rec read_seq(const Args& a, int b) {
+  Rec r;
+  r.b = b;
+  r.base = 0;
+  r.ref = 0;
+  r.low = 0;
+  r.pre = 0;
+  r.units = r.n = r.tail = r.e1 = r.e2 = r.masked = 0;
+  const int n = a.n_entries[b];
+  if (n == 0 || malformed(a, b)) return r;
+  r.n = n;
+  r.tail = a.tail_len[b];
+  const int32_t* pos = a.block_pos ? a.block_pos + static_cast<long long>(b) * a.bt_stride : nullptr;
+  const long long last = pos ? pos[n - 1] : n - 1;
+  const long long x_b = last * PAGE + r.tail - 1;
+  long long low = a.doc_start ? a.doc_start[b] : 0;
+  if (a.window > 0 && x_b - a.window + 1 > low) low = x_b - a.window + 1;
+  const int pre = a.prefix_len ? a.prefix_len[b] : 0;
+  if (low > pre && low > 0) {
+    r.masked = 1;
+    r.low = low;
+    r.pre = pre < 0 ? 0 : pre;
+    r.e2 = first_at_least(pos, n, low >> 6);              // its last position >= low
+    r.e1 = first_at_least(pos, n, (static_cast<long long>(r.pre) + PAGE - 1) >> 6);
+    if (r.e1 > r.e2) r.e1 = r.e2;                         // one entry holds both bounds
+  }
+  const int seen = r.e1 + n - r.e2;
+  if (seen > 0) {
+    const int j = r.e2 < n ? n - 1 : r.e1 - 1;            // last seen entry
+    r.ref = (pos ? static_cast<long long>(pos[j]) : j) * PAGE + PAGE - 1;
+    r.units = 2 * seen - (j == n - 1 && r.tail <= UNIT ? 1 : 0);
+  }
+  return r;
+}
+
+// Entry of the seen unit u.
+__device__ __forceinline__ int unit_entry(const Rec& r, int u) {
+  const int v = u >> 1;
+  return v < r.e1 ? v : r.e2 + v - r.e1;
+}
+
+// A piece of one (sequence, key head) pair held by one CTA: units [u0, u1).
+struct Seg {
+  int kvh, u0, u1;
+};
+
+// Walks the segments of a record inside the CTA's units [us, ue); every role walks the same.
+struct SegWalk {
+  long long cur, end;
+  __device__ __forceinline__ void start(const Rec& r, long long us, long long ue, int Hkv) {
+    cur = us > r.base ? us : r.base;
+    const long long e = r.base + static_cast<long long>(Hkv) * r.units;
+    end = ue < e ? ue : e;
+  }
+  __device__ __forceinline__ bool next(const Rec& r, Seg& s) {
+    if (cur >= end) return false;
+    const long long rel = cur - r.base;
+    s.kvh = static_cast<int>(rel / r.units);
+    s.u0 = static_cast<int>(rel - static_cast<long long>(s.kvh) * r.units);
+    const long long left = end - cur;
+    s.u1 = left < r.units - s.u0 ? s.u0 + static_cast<int>(left) : r.units;
+    cur += s.u1 - s.u0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int seg_tiles(const Seg& s) { return (s.u1 - s.u0 + 3) >> 2; }
+
+// Units [t0, t1) of tile t, newest tile first. The partial tile (fewer than 4 units) is
+// tile 0: its small loads overlap the pipeline fill.
+__device__ __forceinline__ void tile_units(const Seg& s, int t, int& t0, int& t1) {
+  const int len = s.u1 - s.u0;
+  const int first = (len & 3) ? (len & 3) : 4;
+  t1 = t == 0 ? s.u1 : s.u1 - first - 4 * (t - 1);
+  t0 = t == 0 ? s.u1 - first : t1 - 4;
+}
+
+// Whether a tile may hold rows that are loaded but not seen: the end of the tail page and
+// the entries at the masks' bounds. Every role gives the same answer.
+__device__ __forceinline__ bool tile_dirty(const Rec& r, int t0, int t1) {
+  if (t1 == r.units && (r.tail & (UNIT - 1)) != 0 && (r.e2 < r.n || r.e1 == r.n)) return true;
+  return r.masked && t1 > 2 * (r.e1 - 1) && t0 < 2 * (r.e1 + 1);
+}
+
+template <int HP>
+struct Misc {
+  uint64_t full[8], empty[8];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full, pv_done, q_full, q_free, clean, mma_done;
+  uint32_t tmem_base;
+  int abort;
+  int nrec, more, ctas;
+  long long U;
+  long long wsum[NTHREADS / 32];
+  Rec rec[MAXREC];
+  int y[YRING];
+  float red[4][HP];
+  __align__(16) float m[HP];       // running max per head (log2 units), 0 while nothing was seen
+  __align__(16) float alpha[HP];
+  __align__(16) float slope[HP];   // slope * log2 e
+  float m_raw[HP];                 // running max, -inf while nothing was seen
+};
+
+// Exclusive prefix over the CTA's threads; *total receives the sum.
+template <int HP>
+__device__ __forceinline__ long long block_scan(long long v, Misc<HP>* m, int tid, long long* total) {
+  const int lane = tid & 31, warp = tid >> 5;
+  long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();
+  if (lane == 31) m->wsum[warp] = incl;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    const long long t = m->wsum[w];
+    if (w < warp) before += t;
+    sum += t;
+  }
+  *total = sum;
+  return before + incl - v;
+}
+
+// All threads: the batch's units, this CTA's range of them, and the records that meet it,
+// without the first `skip`. CTA 0 also writes the plan for the joining kernel (skip 0).
+template <int HP>
+__device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int tid, long long& us,
+                                      long long& ue) {
+  const bool one = a.B <= NTHREADS;       // one sequence per thread: read it once
+  Rec r;
+  r.units = 0;
+  long long base0 = 0, units = 0;
+  if (one) {
+    if (tid < a.B) r = read_seq(a, tid);
+    base0 = block_scan(static_cast<long long>(r.units), m, tid, &units);
+  } else {
+    for (int b0 = 0; b0 < a.B; b0 += NTHREADS)
+      if (b0 + tid < a.B) units += read_seq(a, b0 + tid).units;
+    long long total;
+    block_scan(units, m, tid, &total);
+    units = total;
+  }
+  const long long U = units * a.Hkv;
+  long long want = (U + a.min_units - 1) / a.min_units;
+  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
+  us = ue = 0;
+  if (static_cast<int>(blockIdx.x) < ctas) {
+    us = (static_cast<long long>(blockIdx.x) * U) / ctas;
+    ue = (static_cast<long long>(blockIdx.x + 1) * U) / ctas;
+  }
+  const bool write = blockIdx.x == 0 && skip == 0;
+  if (write && tid == 0) {
+    a.head->U = U;
+    a.head->ctas = ctas;
+  }
+  long long found = 0, base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += NTHREADS) {
+    const int b = b0 + tid;
+    long long ex = base0, total = units;
+    if (!one) {
+      r.units = 0;
+      if (b < a.B) r = read_seq(a, b);
+      ex = block_scan(static_cast<long long>(r.units), m, tid, &total);
+    }
+    const long long first = (base + ex) * a.Hkv;
+    base += total;
+    if (b < a.B) {
+      r.base = first;
+      if (write) {
+        if (malformed(a, b)) set_err(a.err, LSA_DEVERR_BAD_SIZE);
+        Plan p;
+        p.base = first;
+        p.units = r.units;
+        p.n = r.n;
+        p.e1 = r.e1;
+        p.e2 = r.e2;
+        p.tail = r.tail;
+        p.pad = 0;
+        a.plan[b] = p;
+      }
+    }
+    const bool hit = b < a.B && r.units > 0 && first < ue &&
+                     first + static_cast<long long>(a.Hkv) * r.units > us;
+    long long hits;
+    const long long idx = found + block_scan(hit ? 1ll : 0ll, m, tid, &hits) - skip;
+    if (hit && idx >= 0 && idx < MAXREC) m->rec[idx] = r;
+    found += hits;
+  }
+  if (tid == 0) {
+    const long long left = found - skip;
+    m->nrec = static_cast<int>(left > MAXREC ? MAXREC : left < 0 ? 0 : left);
+    m->more = left > MAXREC;
+    m->ctas = ctas;
+    m->U = U;
+  }
+  __syncthreads();
+}
+
+// Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
+// stage count is even. Up to 32 heads two CTAs share an SM (at most 113 KB each), so that one
+// CTA's softmax overlaps the other's products; 64 heads need a whole SM.
+template <int HP, int NDC>
+struct Layout {
+  static constexpr int NDB = NDC / 2;
+  static constexpr int CTAS_PER_SM = HP <= 32 ? 2 : 1;
+  static constexpr int Q_BYTES = NDC * HP * 128;      // [NDC][HP][64]
+  static constexpr int P_ROW = HP * 2;                // bytes of a token's row of P
+  static constexpr int P_BYTES = TILE * P_ROW;
+  static constexpr int FIXED = Q_BYTES + P_BYTES + static_cast<int>(sizeof(Misc<HP>)) + 1024;
+  static constexpr int BUDGET = HP <= 32 ? 115712 : 232448;
+  static constexpr int NST_MAX = (BUDGET - FIXED) / STAGE_BYTES / 2 * 2;
+  static constexpr int NST = NST_MAX > 8 ? 8 : NST_MAX;
+  static constexpr int RING_BYTES = NST * STAGE_BYTES;
+  static constexpr int RING_OFF = Q_BYTES;            // Q and ring bases: multiples of 1024
+  static constexpr int P_OFF = RING_OFF + RING_BYTES;
+  static constexpr int MISC_OFF = P_OFF + P_BYTES;
+  static constexpr int SMEM = MISC_OFF + static_cast<int>(sizeof(Misc<HP>)) + 1024;
+  static constexpr int TMEM_USED = 2 * HP + NDB * HP;
+  static constexpr uint32_t TMEM_COLS =
+      TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
+  static_assert(NST >= 4 && SMEM <= BUDGET, "shared memory");
+  static_assert(TMEM_USED * CTAS_PER_SM <= 512 && static_cast<int>(TMEM_COLS) * CTAS_PER_SM <= 512,
+                "tensor memory");
+};
+
+// Byte of granule c (16 bytes) of row r of P: the granule index is XOR-ed with the bits of
+// the row that its swizzle (32, 64 or 128 bytes, the row size) takes.
+template <int HP>
+__device__ __forceinline__ uint32_t p_offset(uint32_t row, uint32_t c) {
+  if constexpr (HP == 64) return row * 128u + ((c ^ (row & 7u)) << 4);
+  if constexpr (HP == 32) return row * 64u + ((c ^ ((row >> 1) & 3u)) << 4);
+  return row * 32u + ((c ^ ((row >> 2) & 1u)) << 4);
+}
+
+// Descriptor of P at token k of the tile: MN-major, HP heads in one swizzle atom, 8-token
+// groups one atom apart.
+template <int HP>
+__device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
+  constexpr uint64_t layout = HP == 64 ? 2 : HP == 32 ? 4 : 6;   // 128-, 64-, 32-byte swizzle
+  constexpr uint32_t atom = 8u * HP * 2u;
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(atom >> 4) << 16;
+  d |= static_cast<uint64_t>(atom >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= layout << 61;
+  return d;
+}
+
+// tanh(t) * c for the capped scores. tanh t = 1 - 2 / (1 + 2^(2 t log2 e)) is off by a few
+// 2^-24 in absolute terms; where |t| < 1/16 that is much of the result, and the Taylor
+// series t (1 - t^2/3 + 2 t^4/15) is used (relative error below 17/315 t^6 < 4e-9).
+__device__ __forceinline__ float cap_tanh(float t, float c) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(2.f * LOG2E * t)));
+  const float big = fmaf(-2.f, r, 1.f);
+  const float t2 = t * t;
+  const float small = t * fmaf(t2, fmaf(t2, 2.f / 15.f, -1.f / 3.f), 1.f);
+  return c * (fabsf(t) < 0.0625f ? small : big);
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
+  uint32_t w;
+  if (f16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+__device__ __forceinline__ uint16_t to16(float v, bool f16) {
+  return static_cast<uint16_t>(pack16(v, 0.f, f16) & 0xffffu);
+}
+
+template <int HP, int NDC>
+__global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map_kv,
+                      const __grid_constant__ CUtensorMap map_q, const __grid_constant__ Args a) {
+  using LY = Layout<HP, NDC>;
+  constexpr int NDB = LY::NDB, NST = LY::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + LY::RING_OFF;
+  uint8_t* sP = smem + LY::P_OFF;
+  Misc<HP>* m = reinterpret_cast<Misc<HP>*>(smem + LY::MISC_OFF);
+  volatile int* abort = &m->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.G;
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&m->full[i], 1);
+      mbar_init(&m->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m->s_full[i], 1);
+      mbar_init(&m->s_free[i], 4);   // one arrival per softmax warp
+    }
+    mbar_init(&m->p_full, 4);
+    mbar_init(&m->pv_done, 1);
+    mbar_init(&m->q_full, 1);
+    mbar_init(&m->q_free, 1);
+    mbar_init(&m->clean, 4);
+    mbar_init(&m->mma_done, 1);
+    m->abort = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&map_kv);
+    prefetch_tensormap(&map_q);
+  }
+  if (warp == 1) {
+    tmem_alloc(&m->tmem_base, LY::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // rows of the padded heads: zeros, so that their scores are 0 and need no masks
+  for (int i = tid; i < NDC * (HP - G) * 8; i += NTHREADS) {
+    const int c = i / ((HP - G) * 8), k = i - c * (HP - G) * 8;
+    *reinterpret_cast<uint4*>(sQ + c * HP * 128 + G * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  // Launched as a programmatic dependent: nothing a preceding kernel may write is read or
+  // written before this point.
+  grid_dependency_wait();
+  grid_dependents_launch();
+  long long us, ue;
+  plan_cta<HP>(a, 0, m, tid, us, ue);      // ends with a block-wide barrier
+  tc_fence_after();
+  const uint32_t tmem = m->tmem_base;
+
+  int ring_pos = 0;      // stages armed (producer) or consumed (MMA); softmax: stages before the segment
+  int seg_count = 0;     // segments started by this role
+  int gtile_s = 0;       // S tiles issued / read
+  int gtile_o = 0;       // PV tiles issued / P tiles written
+  int n_clean = 0;       // V stage pairs cleared so far
+  for (int batch = 0;; ++batch) {
+    const int nrec = m->nrec;
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer
+      const uint64_t evict_first = l2_policy_evict_first();
+      const int y_out = static_cast<int>(a.n_pages * 2 * a.Hkv * PAGE);   // outside the map
+      const int kv_rows = a.Hkv * PAGE;
+      bool ok = true;
+      for (int ri = 0; ri < nrec && ok; ++ri) {
+        const Rec& r = m->rec[ri];
+        const int32_t* bt = a.block_table + static_cast<long long>(r.b) * a.bt_stride;
+        SegWalk walk;
+        Seg sg;
+        walk.start(r, us, ue, a.Hkv);
+        while (ok && walk.next(r, sg)) {
+          const int T = seg_tiles(sg), len = sg.u1 - sg.u0;
+          if (lane == 0) {
+            if (seg_count > 0) ok = mbar_wait(&m->q_free, (seg_count - 1) & 1, abort);
+            if (ok) {
+              mbar_arrive_expect_tx(&m->q_full, NDC * G * 128);
+              for (int c = 0; c < NDC; ++c)
+                tma_load_2d(sQ + c * HP * 128, &map_q, &m->q_full, 64 * c, r.b * a.H + sg.kvh * G);
+              ++seg_count;
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          int filled = 0;                 // units of the segment looked up, newest first
+          for (int i = 0; i <= T && ok; ++i) {
+            int t0, t1;
+            tile_units(sg, i, t0, t1);
+            if (i < T && sg.u1 - t0 > filled) {
+              // the pool rows of the next 128 units, by all lanes
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < YRING / 64; ++e) {
+                const int k = filled + 32 * e + lane;
+                if (k < len) {
+                  const int u = sg.u1 - 1 - k;
+                  const int page = bt[unit_entry(r, u)];
+                  int y = -1;
+                  if (page < 0 || page >= a.n_pages)
+                    set_err(a.err, LSA_DEVERR_BAD_PAGE);
+                  else
+                    y = (page * 2 * a.Hkv + sg.kvh) * PAGE + (u & 1) * UNIT;
+                  m->y[k & (YRING - 1)] = y;
+                }
+              }
+              filled += YRING / 2;
+              __syncwarp();
+            }
+            if (lane == 0) {
+              for (int kv = 0; kv < 2 && ok; ++kv) {
+                // stage order per step i: K of tile i, then V of tile i-1
+                const int tile = kv == 0 ? i : i - 1;
+                if (tile < 0 || tile >= T) continue;
+                tile_units(sg, tile, t0, t1);
+                int ys[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  // rows past the tile's units and bad pages: a box outside the map, which
+                  // the copy engine fills with zeros without reading memory
+                  const int u = t0 + x;
+                  const int y = u < t1 ? m->y[(sg.u1 - 1 - u) & (YRING - 1)] : -1;
+                  ys[x] = y < 0 ? y_out : y + kv * kv_rows;
+                }
+                for (int c = 0; c < NDC; ++c) {
+                  const int st = ring_pos % NST;
+                  ok = mbar_wait(&m->empty[st], ((ring_pos / NST) & 1) ^ 1, abort);
+                  if (!ok) break;
+                  mbar_arrive_expect_tx(&m->full[st], STAGE_BYTES);
+                  uint8_t* dst = sRing + st * STAGE_BYTES;
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    tma_load_2d_hint(dst + x * (UNIT * 128), &map_kv, &m->full[st], 64 * c, ys[x],
+                                     evict_first);
+                  ++ring_pos;
+                }
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        // operand format fields: 1 = bf16 (set by idesc_bf16_f32), 0 = fp16
+        const uint32_t fmt = a.f16 ? ~((1u << 7) | (1u << 10)) : ~0u;
+        const uint32_t idesc_s = idesc_bf16_f32(128, HP, false, false) & fmt;
+        const uint32_t idesc_o = idesc_bf16_f32(128, HP, true, true) & fmt;
+        const uint32_t q_base = smem_u32(sQ), p_base = smem_u32(sP), ring_base = smem_u32(sRing);
+        bool ok = true;
+        for (int ri = 0; ri < nrec && ok; ++ri) {
+          const Rec& r = m->rec[ri];
+          SegWalk walk;
+          Seg sg;
+          walk.start(r, us, ue, a.Hkv);
+          while (ok && walk.next(r, sg)) {
+            const int T = seg_tiles(sg);
+            ok = mbar_wait(&m->q_full, seg_count & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            ++seg_count;
+            for (int i = 0; i <= T && ok; ++i) {
+              if (i < T) {
+                const int sb = gtile_s & 1;
+                if (gtile_s >= 2 && !mbar_wait(&m->s_free[sb], ((gtile_s >> 1) - 1) & 1, abort)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                const uint32_t d_s = tmem + sb * HP;
+                for (int kb = 0; kb < NDC; ++kb) {
+                  const int st = ring_pos % NST;
+                  if (!mbar_wait(&m->full[st], (ring_pos / NST) & 1, abort)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                  const uint32_t sa = ring_base + st * STAGE_BYTES;
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(d_s, sdesc_sw128(sa + kk * 32, 16, 1024),
+                              sdesc_sw128(q_base + kb * HP * 128 + kk * 32, 16, 1024), idesc_s,
+                              (kb | kk) != 0);
+                  umma_commit(&m->empty[st]);
+                  ++ring_pos;
+                }
+                if (!ok) break;
+                umma_commit(&m->s_full[sb]);
+                if (i == T - 1) umma_commit(&m->q_free);
+                ++gtile_s;
+              }
+              if (i >= 1) {
+                const int j = i - 1;
+                int t0, t1;
+                tile_units(sg, j, t0, t1);
+                const bool dirty = tile_dirty(r, t0, t1);
+                if (!mbar_wait(&m->p_full, gtile_o & 1, abort)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                for (int db = 0; db < NDB; ++db) {
+                  const int st0 = ring_pos % NST;   // even: the pair (st0, st0 + 1) is adjacent
+                  if (dirty) {
+                    ok = mbar_wait(&m->clean, n_clean & 1, abort);
+                    ++n_clean;
+                  }
+                  if (!ok || !mbar_wait(&m->full[st0], (ring_pos / NST) & 1, abort) ||
+                      !mbar_wait(&m->full[st0 + 1], (ring_pos / NST) & 1, abort)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                  const uint32_t sa = ring_base + st0 * STAGE_BYTES;
+                  const uint32_t d_o = tmem + 2 * HP + db * HP;
+#pragma unroll
+                  for (int kk = 0; kk < TILE / 16; ++kk)
+                    umma_bf16(d_o, sdesc_sw128(sa + kk * 16 * 128, STAGE_BYTES, 1024),
+                              p_desc<HP>(p_base + kk * 16 * LY::P_ROW), idesc_o,
+                              (j > 0 || kk > 0) ? 1u : 0u);
+                  umma_commit(&m->empty[st0]);
+                  umma_commit(&m->empty[st0 + 1]);
+                  ring_pos += 2;
+                }
+                if (!ok) break;
+                umma_commit(&m->pv_done);
+                ++gtile_o;
+              }
+            }
+          }
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- softmax
+      // Every wait result is folded into the next barrier with reduction, so the four warps
+      // leave together and no named barrier is left half-arrived.
+      const int sw = warp & 3;                   // TMEM lanes, and unit of the tile, of this warp
+      const int t128 = tid - 64;
+      const uint32_t row = sw * 32 + lane;       // token row of the tile
+      const uint32_t lane_addr = static_cast<uint32_t>(sw * 32) << 16;
+      const bool f16 = a.f16 != 0;
+      const float scale2 = a.cap > 0.f ? a.scale / a.cap : a.scale * LOG2E;
+      const float cap2 = a.cap * LOG2E;
+      constexpr int HL = HP >= 32 ? HP / 32 : 1;  // heads whose sums a lane holds
+      const int h_lane = HP >= 32 ? lane * HL : lane >> 1;
+      bool failed = false;
+      for (int ri = 0; ri < nrec && !failed; ++ri) {
+        const Rec& r = m->rec[ri];
+        const int32_t* bt = a.block_table + static_cast<long long>(r.b) * a.bt_stride;
+        const int32_t* bp = a.block_pos ? a.block_pos + static_cast<long long>(r.b) * a.bt_stride : nullptr;
+        SegWalk walk;
+        Seg sg;
+        walk.start(r, us, ue, a.Hkv);
+        while (!failed && walk.next(r, sg)) {
+          const int T = seg_tiles(sg);
+          const int h0 = sg.kvh * G;
+          if (t128 < HP) {
+            m->m[t128] = 0.f;
+            m->m_raw[t128] = -INFINITY;
+            m->slope[t128] = a.slopes != nullptr && t128 < G ? a.slopes[h0 + t128] * LOG2E : 0.f;
+          }
+          float l[HL];
+#pragma unroll
+          for (int i = 0; i < HL; ++i) l[i] = 0.f;
+          // this warp's unit of the next tile is looked up one tile ahead
+          int t0, t1;
+          tile_units(sg, 0, t0, t1);
+          int page_n = -1, pos_n = 0;
+          if (t0 + sw < t1) {
+            const int e = unit_entry(r, t0 + sw);
+            page_n = bt[e];
+            pos_n = bp ? bp[e] : e;
+          }
+          named_bar_sync(1, 128);
+          for (int j = 0; j < T; ++j) {
+            tile_units(sg, j, t0, t1);
+            const bool dirty = tile_dirty(r, t0, t1);
+            const int u = t0 + sw;
+            const int page = page_n;
+            const long long x0 = static_cast<long long>(pos_n) * PAGE + (u & 1) * UNIT + lane;
+            if (j + 1 < T) {
+              int n0, n1;
+              tile_units(sg, j + 1, n0, n1);
+              const int e = unit_entry(r, n0 + sw);      // tiles after the first hold 4 units
+              page_n = bt[e];
+              pos_n = bp ? bp[e] : e;
+            }
+            bool seen = u < t1 && page >= 0 && page < a.n_pages;
+            const int entry = u < t1 ? unit_entry(r, u) : 0;
+            if (seen && entry == r.n - 1) seen = (u & 1) * UNIT + lane < r.tail;
+            if (seen && r.masked) seen = x0 < r.pre || x0 >= r.low;
+            const bool all_seen = __all_sync(0xffffffffu, seen);
+            const int sb = gtile_s & 1;
+            if (!failed)
+              failed = !__all_sync(0xffffffffu, mbar_wait(&m->s_full[sb], (gtile_s >> 1) & 1, abort));
+            tc_fence_after();
+            float x[HP];
+            bool over = false;
+            if (!failed) {
+              tmem_ld_row<HP>(tmem + lane_addr + sb * HP, x);
+              tmem_wait_ld();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&m->s_free[sb]);
+              if (a.cap > 0.f) {
+#pragma unroll
+                for (int h = 0; h < HP; ++h) x[h] = cap_tanh(x[h] * scale2, cap2);
+              } else {
+#pragma unroll
+                for (int h = 0; h < HP; ++h) x[h] *= scale2;
+              }
+              if (a.slopes != nullptr) {
+                const float rel = static_cast<float>(x0 - r.ref);
+#pragma unroll
+                for (int h = 0; h < HP; h += 4) {
+                  const float4 s = *reinterpret_cast<const float4*>(m->slope + h);
+                  x[h] = fmaf(s.x, rel, x[h]);
+                  x[h + 1] = fmaf(s.y, rel, x[h + 1]);
+                  x[h + 2] = fmaf(s.z, rel, x[h + 2]);
+                  x[h + 3] = fmaf(s.w, rel, x[h + 3]);
+                }
+              }
+              if (!all_seen) {
+#pragma unroll
+                for (int h = 0; h < HP; ++h) x[h] = seen ? x[h] : -INFINITY;
+              }
+              if (j == 0) {
+                over = true;             // the segment's first tile sets the running max
+              } else {
+#pragma unroll
+                for (int h = 0; h < HP; h += 4) {
+                  const float4 mm = *reinterpret_cast<const float4*>(m->m + h);
+                  over |= x[h] > mm.x + RESCALE_LOG2 || x[h + 1] > mm.y + RESCALE_LOG2 ||
+                          x[h + 2] > mm.z + RESCALE_LOG2 || x[h + 3] > mm.w + RESCALE_LOG2;
+                }
+              }
+            }
+            ++gtile_s;
+            // one vote: bit 0 of the barrier's OR says that some wait failed or some score is over
+            const bool any = named_bar_any(1, 128, failed || over);
+            if (any) {
+              if (named_bar_any(1, 128, failed)) {
+                failed = true;
+                break;
+              }
+              float c[HP];
+#pragma unroll
+              for (int h = 0; h < HP; ++h) c[h] = x[h];
+              warp_reduce_scatter<HP, true>(c, lane);
+              store_scattered<HP>(m->red[sw], c, lane);
+              named_bar_sync(1, 128);
+              if (t128 < HP) {
+                const int h = t128;
+                const float top = fmaxf(fmaxf(m->red[0][h], m->red[1][h]), fmaxf(m->red[2][h], m->red[3][h]));
+                const float old = m->m_raw[h];
+                float al = 1.f;
+                // an unset max (-inf) takes any score; sums kept so far were then all 0
+                if (top > old + RESCALE_LOG2 || (old == -INFINITY && top > old)) {
+                  al = exp2f(old - top);
+                  m->m_raw[h] = top;
+                  m->m[h] = top;
+                }
+                m->alpha[h] = al;
+              }
+              named_bar_sync(1, 128);
+#pragma unroll
+              for (int i = 0; i < HL; ++i) l[i] *= m->alpha[h_lane + i];
+            }
+            // weights; their fp32 sums per unit and head
+            uint32_t pw[HP / 2];
+#pragma unroll
+            for (int h = 0; h < HP; h += 4) {
+              const float4 mm = *reinterpret_cast<const float4*>(m->m + h);
+              x[h] = ex2_approx(x[h] - mm.x);
+              x[h + 1] = ex2_approx(x[h + 1] - mm.y);
+              x[h + 2] = ex2_approx(x[h + 2] - mm.z);
+              x[h + 3] = ex2_approx(x[h + 3] - mm.w);
+            }
+            // P is rounded to the operands' type, which the product needs (at most half an ulp of
+            // each weight); the sums take the weights as they were before
+            if (f16) {
+#pragma unroll
+              for (int h = 0; h < HP; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], true);
+            } else {
+#pragma unroll
+              for (int h = 0; h < HP; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], false);
+            }
+            warp_reduce_scatter<HP, false>(x, lane);
+#pragma unroll
+            for (int i = 0; i < HL; ++i) l[i] += x[i];
+            if (a.score != nullptr && u < t1) {
+              float2* uw = a.unit_w + ((static_cast<long long>(r.b) * a.bt_stride + entry) * 2 + (u & 1)) * a.H + h0;
+              if (HP >= 32 || (lane & 1) == 0) {
+#pragma unroll
+                for (int i = 0; i < HL; ++i)
+                  if (h_lane + i < G) uw[h_lane + i] = make_float2(x[i], m->m[h_lane + i]);
+              }
+            }
+            // the previous tile's product must be done before P is overwritten or O rescaled
+            if (gtile_o >= 1)
+              failed = !__all_sync(0xffffffffu, mbar_wait(&m->pv_done, (gtile_o - 1) & 1, abort));
+            if (failed) continue;                // the next vote tells all warps
+            tc_fence_after();
+            if (any && j > 0) {
+#pragma unroll
+              for (int db = 0; db < NDB; ++db) {
+#pragma unroll
+                for (int c = 0; c < HP / 16; ++c) {
+                  const uint32_t ta = tmem + lane_addr + 2 * HP + db * HP + 16 * c;
+                  float o[16];
+                  tmem_ld16(ta, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] *= m->alpha[16 * c + i];
+                  tmem_st16(ta, o);
+                }
+              }
+              tmem_wait_st();
+            }
+#pragma unroll
+            for (int c = 0; c < HP / 8; ++c)
+              *reinterpret_cast<uint4*>(sP + p_offset<HP>(row, c)) =
+                  make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->p_full);
+            ++gtile_o;
+            if (dirty) {
+              // Clear the rows that are not seen in each pair of V stages as it arrives. A wait on
+              // a stage's phase is sound only when the phase before it is complete: the next
+              // tile's K stages come before this V in the ring, so their product is awaited.
+              if (j + 1 < T)
+                failed = !__all_sync(0xffffffffu, mbar_wait(&m->s_full[gtile_s & 1], (gtile_s >> 1) & 1, abort));
+              int pos = ring_pos + (j + 1 < T ? (2 * j + 2) * NDC : (2 * T - 1) * NDC);
+              for (int db = 0; db < NDB && !failed; ++db, pos += 2) {
+                bool got = true;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                  const int st = (pos + s) % NST;
+                  got = got && mbar_wait(&m->full[st], ((pos + s) / NST) & 1, abort);
+                  if (got && !seen) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                      *reinterpret_cast<uint4*>(sRing + st * STAGE_BYTES + row * 128 + c * 16) =
+                          make_uint4(0, 0, 0, 0);
+                  }
+                }
+                failed = !__all_sync(0xffffffffu, got);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && !failed) mbar_arrive(&m->clean);
+              }
+            }
+          }
+          if (named_bar_any(1, 128, failed)) {
+            failed = true;
+            break;
+          }
+          ring_pos += 2 * T * NDC;
+          // ------------------------------------------------------- segment epilogue
+          failed = !__all_sync(0xffffffffu, mbar_wait(&m->pv_done, (gtile_o - 1) & 1, abort));
+          tc_fence_after();
+          if (HP >= 32 || (lane & 1) == 0) {
+#pragma unroll
+            for (int i = 0; i < HL; ++i) m->red[sw][h_lane + i] = l[i];
+          }
+          if (named_bar_any(1, 128, failed)) {
+            failed = true;
+            break;
+          }
+          // a pair held whole by this CTA is normalised and written out here; a split one
+          // leaves its part in slot CTA + pair. The (max, sum) pairs of both go to the
+          // workspace: the pages' weights are normalised by them.
+          const bool whole = sg.u0 == 0 && sg.u1 == r.units;
+          const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(r.b) * a.Hkv + sg.kvh;
+          if (t128 < G) {
+            const float sum = m->red[0][t128] + m->red[1][t128] + m->red[2][t128] + m->red[3][t128];
+            a.part_ml[slot * G + t128] = make_float2(m->m_raw[t128], sum);
+            m->alpha[t128] = sum == 0.f ? 0.f : 1.f / sum;
+          }
+          named_bar_sync(1, 128);
+          uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0) * a.d + row;
+          float* po = a.part_o + slot * G * a.d + row;
+#pragma unroll 1
+          for (int db = 0; db < NDB; ++db) {
+            float o[HP];
+            tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
+            tmem_wait_ld();
+            if (whole) {
+#pragma unroll
+              for (int h = 0; h < HP; ++h)
+                if (h < G) fo[h * a.d + db * 128] = to16(o[h] * m->alpha[h], f16);
+            } else {
+#pragma unroll
+              for (int h = 0; h < HP; ++h)
+                if (h < G) po[h * a.d + db * 128] = o[h];
+            }
+          }
+          tc_fence_before();
+          named_bar_sync(1, 128);
+        }
+      }
+    }
+    // ------------------------------------------------------------ next records
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (!m->more || *abort) break;
+    __syncthreads();
+    plan_cta<HP>(a, (batch + 1) * MAXREC, m, tid, us, ue);
+  }
+  // ---------------------------------------------------------------- teardown
+  if (*abort) {
+    if (tid == 0) set_err(a.err, LSA_DEVERR_TIMEOUT);
+    // the producer waits (bounded) for its own copies still in flight
+    if (warp == 0 && lane == 0) {
+      for (int k = max(0, ring_pos - NST); k < ring_pos; ++k)
+        mbar_wait(&m->full[k % NST], (k / NST) & 1, nullptr);
+      if (seg_count > 0) mbar_wait(&m->q_full, (seg_count - 1) & 1, nullptr);
+    }
+    // the MMA thread waits (bounded) for its own tensor-core work
+    if (warp == 1 && lane == 0) {
+      umma_commit(&m->mma_done);
+      mbar_wait(&m->mma_done, 0, nullptr);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, LY::TMEM_COLS);
+}
+
+// ------------------------------------------------------------------------ joining
+// CTA holding unit u of the split: the largest c with floor(c * U / ctas) <= u.
+__device__ __forceinline__ int cta_of_unit(long long u, long long U, long long ctas) {
+  return static_cast<int>(((u + 1) * ctas - 1) / U);
+}
+
+struct JoinArgs {
+  int out_blocks;    // blocks that join outputs; the rest add the pages' weights
+  int wide;          // a block per (sequence, head, 128 dims); else a warp per (sequence, head)
+  int entries;       // table entries per block of the second kind
+  int chunks;        //   and such blocks per sequence
+};
+
+// out[b][h][cols] = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the n parts of a head,
+// by `groups` groups of threads that take every groups-th part; each thread holds 4 dims.
+__device__ __forceinline__ float4 join_parts(const float* part, const float* w, int n, int first, int step,
+                                             long long stride) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = first; k < n; k += step) {
+    const float4 v = *reinterpret_cast<const float4*>(part + k * stride);
+    const float wk = w[k];
+    // a part of weight 0 saw nothing: its values are dropped whatever they are
+    if (wk != 0.f) {
+      acc.x = fmaf(wk, v.x, acc.x);
+      acc.y = fmaf(wk, v.y, acc.y);
+      acc.z = fmaf(wk, v.z, acc.z);
+      acc.w = fmaf(wk, v.w, acc.w);
+    }
+  }
+  return acc;
+}
+
+__device__ __forceinline__ void store_out(uint16_t* p, float4 v, float inv, bool f16) {
+  uint2 w;
+  w.x = pack16(v.x * inv, v.y * inv, f16);
+  w.y = pack16(v.z * inv, v.w * inv, f16);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+
+__global__ void __launch_bounds__(JOIN_THREADS)
+    paged_join_kernel(const __grid_constant__ Args a, const __grid_constant__ JoinArgs ja) {
+  extern __shared__ float sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.G;
+  const bool f16 = a.f16 != 0;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long U = a.head->U;
+  const long long ctas = a.head->ctas;
+  if (static_cast<int>(blockIdx.x) < ja.out_blocks) {
+    if (ja.wide) {
+      // -------- a block per (sequence, head, 128 dims): parts split over 8 groups of 32 threads
+      const int chunks = a.d / 128;
+      const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
+      const int b = item / a.H, h = item - b * a.H;
+      const Plan p = a.plan[b];
+      uint16_t* out = a.out + (static_cast<long long>(b) * a.H + h) * a.d + chunk * 128 + lane * 4;
+      const int kvh = h / G;
+      int n = 0, c0 = 0;
+      if (p.units > 0) {
+        const long long v0 = p.base + static_cast<long long>(kvh) * p.units;
+        c0 = cta_of_unit(v0, U, ctas);
+        n = cta_of_unit(v0 + p.units - 1, U, ctas) - c0 + 1;
+      }
+      if (n == 1) return;                       // written by the CTA that held it whole
+      if (n == 0) {
+        if (warp == 0) store_out(out, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, f16);
+        return;
+      }
+      const long long slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
+      const float2* ml = a.part_ml + slot * G + (h - kvh * G);
+      float* w = sm;                            // [n]
+      float4* acc_s = reinterpret_cast<float4*>(sm + MAX_CTAS);
+      float* red = sm + MAX_CTAS + 4 * JOIN_THREADS;
+      float mx = -INFINITY;
+      float2 mine[MAX_CTAS / JOIN_THREADS];
+#pragma unroll
+      for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
+        const int k = tid + i * JOIN_THREADS;
+        mine[i] = k < n ? ml[static_cast<long long>(k) * G] : make_float2(-INFINITY, 0.f);
+        mx = fmaxf(mx, mine[i].x);
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (lane == 0) red[warp] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < JOIN_THREADS / 32; ++i) mx = fmaxf(mx, red[i]);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
+        const int k = tid + i * JOIN_THREADS;
+        const float wk = mine[i].x == -INFINITY ? 0.f : exp2f(mine[i].x - mx);
+        if (k < n) w[k] = wk;
+        sum += wk == 0.f ? 0.f : wk * mine[i].y;
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) red[8 + warp] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < JOIN_THREADS / 32; ++i) sum += red[8 + i];
+      const float* part = a.part_o + (slot * G + (h - kvh * G)) * a.d + chunk * 128 + lane * 4;
+      acc_s[tid] = join_parts(part, w, n, warp, JOIN_THREADS / 32, static_cast<long long>(G) * a.d);
+      __syncthreads();
+      if (warp == 0) {
+        float4 t = acc_s[lane];
+#pragma unroll
+        for (int i = 1; i < JOIN_THREADS / 32; ++i) {
+          const float4 v = acc_s[i * 32 + lane];
+          t.x += v.x;
+          t.y += v.y;
+          t.z += v.z;
+          t.w += v.w;
+        }
+        store_out(out, t, sum == 0.f ? 0.f : 1.f / sum, f16);
+      }
+      return;
+    }
+    // -------- a warp per (sequence, head)
+    const long long item = static_cast<long long>(blockIdx.x) * (JOIN_THREADS / 32) + warp;
+    if (item >= static_cast<long long>(a.B) * a.H) return;
+    const int b = static_cast<int>(item / a.H), h = static_cast<int>(item - static_cast<long long>(b) * a.H);
+    const Plan p = a.plan[b];
+    uint16_t* out = a.out + item * a.d;
+    const int kvh = h / G;
+    int n = 0, c0 = 0;
+    if (p.units > 0) {
+      const long long v0 = p.base + static_cast<long long>(kvh) * p.units;
+      c0 = cta_of_unit(v0, U, ctas);
+      n = cta_of_unit(v0 + p.units - 1, U, ctas) - c0 + 1;
+    }
+    if (n == 1) return;
+    if (n == 0) {
+      for (int c = lane * 4; c < a.d; c += 128) store_out(out + c, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, f16);
+      return;
+    }
+    const long long slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
+    const float2* ml = a.part_ml + slot * G + (h - kvh * G);
+    float* w = sm + warp * MAX_CTAS;
+    float mx = -INFINITY;
+    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, ml[static_cast<long long>(k) * G].x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float sum = 0.f;
+    for (int k = lane; k < n; k += 32) {
+      const float2 v = ml[static_cast<long long>(k) * G];
+      const float wk = v.x == -INFINITY ? 0.f : exp2f(v.x - mx);
+      w[k] = wk;
+      sum += wk == 0.f ? 0.f : wk * v.y;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float* part = a.part_o + (slot * G + (h - kvh * G)) * a.d;
+    for (int c = lane * 4; c < a.d; c += 128)
+      store_out(out + c, join_parts(part + c, w, n, 0, 1, static_cast<long long>(G) * a.d), inv, f16);
+    return;
+  }
+  // -------- the pages' weights: score = decay * score + sum over heads of
+  // (unit sum) 2^(m_unit - M_h) / L_h, with M_h, L_h over all parts of the head
+  const int blk = blockIdx.x - ja.out_blocks;
+  const int b = blk / ja.chunks, j0 = (blk - b * ja.chunks) * ja.entries;
+  const Plan p = a.plan[b];
+  if (j0 >= p.n) return;
+  float2* fin = reinterpret_cast<float2*>(sm);                 // [H]: (M, 1 / L)
+  float2* tmp = fin + a.H;                                     // [JOIN_THREADS]
+  if (p.units > 0) {
+    // threads over (part, head), heads fastest: consecutive threads read consecutive words
+    const int per = a.H < JOIN_THREADS ? JOIN_THREADS / a.H : 1;   // parts read side by side
+    for (int h0 = 0; h0 < a.H; h0 += JOIN_THREADS) {
+      const int s = a.H < JOIN_THREADS ? tid / a.H : 0;
+      const int h = a.H < JOIN_THREADS ? tid - s * a.H : h0 + tid;
+      float M = -INFINITY, L = 0.f;
+      if (h < a.H && s < per) {
+        const int kvh = h / G;
+        const long long v0 = p.base + static_cast<long long>(kvh) * p.units;
+        const int c0 = cta_of_unit(v0, U, ctas);
+        const int n = cta_of_unit(v0 + p.units - 1, U, ctas) - c0 + 1;
+        const float2* ml = a.part_ml + (c0 + static_cast<long long>(b) * a.Hkv + kvh) * G + (h - kvh * G);
+        // two passes: the max first, so that the sum needs no rescaling (the words are in L1)
+#pragma unroll 4
+        for (int k = s; k < n; k += per) M = fmaxf(M, ml[static_cast<long long>(k) * G].x);
+#pragma unroll 4
+        for (int k = s; k < n; k += per) {
+          const float2 v = ml[static_cast<long long>(k) * G];
+          if (v.y != 0.f) L += v.y * exp2f(v.x - M);
+        }
+      }
+      tmp[tid] = make_float2(M, L);
+      __syncthreads();
+      if (s == 0 && h < a.H) {
+        if (per > 1) {                       // (a.H < JOIN_THREADS)
+          for (int i = 1; i < per; ++i) M = fmaxf(M, tmp[i * a.H + h].x);
+          L = 0.f;
+          for (int i = 0; i < per; ++i) {
+            const float2 v = tmp[i * a.H + h];
+            if (v.y != 0.f) L += v.y * exp2f(v.x - M);
+          }
+        }
+        fin[h] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+      }
+      __syncthreads();
+    }
+  }
+  const int j1 = min(p.n, j0 + ja.entries);
+  for (int j = j0 + warp; j < j1; j += JOIN_THREADS / 32) {
+    const long long at = static_cast<long long>(b) * a.bt_stride + j;
+    float mass = 0.f;
+    if (p.units > 0 && (j < p.e1 || j >= p.e2)) {
+      const int halves = j == p.n - 1 && p.tail <= UNIT ? 1 : 2;
+      const float2* uw = a.unit_w + at * 2 * a.H;
+      for (int h = lane; h < a.H; h += 32) {
+        const float2 f = fin[h];
+        const float2 w0 = uw[h];
+        const float2 w1 = halves == 2 ? uw[a.H + h] : make_float2(0.f, 0.f);
+        if (w0.x != 0.f) mass += w0.x * exp2f(w0.y - f.x) * f.y;
+        if (w1.x != 0.f) mass += w1.x * exp2f(w1.y - f.x) * f.y;
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    }
+    if (lane == 0) a.score[at] = fmaf(a.decay, a.score[at], mass);
+  }
+}
+
+}  // namespace paged
+}  // namespace lsa
+
+// ------------------------------------------------------------------------ host side
+namespace {
+
+using lsa::paged::Args;
+using lsa::paged::JoinArgs;
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct WsLayout {
+  size_t head, plan, ml, o, unit, bytes;
+};
+
+// Slots: one per CTA and one per (sequence, key head) pair.
+WsLayout ws_layout(int B, int H, int Hkv, int d, int bt_stride, bool with_score, int n_sm) {
+  const size_t G = static_cast<size_t>(H) / Hkv;
+  const size_t slots = 2 * static_cast<size_t>(n_sm) + static_cast<size_t>(B) * Hkv;
+  WsLayout w;
+  w.head = 0;
+  w.plan = 256;
+  w.ml = w.plan + up256(static_cast<size_t>(B) * sizeof(lsa::paged::Plan));
+  w.o = w.ml + up256(slots * G * sizeof(float2));
+  w.unit = w.o + up256(slots * G * d * sizeof(float));
+  w.bytes = w.unit + (with_score ? up256(static_cast<size_t>(B) * bt_stride * 2 * H * sizeof(float2)) : 0);
+  return w;
+}
+
+bool valid_shape(int B, int H, int Hkv, int d) {
+  if (B < 1 || B > 65536 || H < 1 || H > 1024 || Hkv < 1 || H % Hkv != 0 || H / Hkv > 64) return false;
+  return d == 128 || d == 256 || d == 384 || d == 512;
+}
+
+template <int HP, int NDC>
+lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_sm, cudaStream_t stream) {
+  using LY = lsa::paged::Layout<HP, NDC>;
+  auto kern = lsa::paged::paged_attn_kernel<HP, NDC>;
+  const lsa_status st = lsa_host::ensure_smem_limit(reinterpret_cast<const void*>(kern), LY::SMEM);
+  if (st != LSA_OK) return st;
+  // at least this many 32-token units per CTA: a CTA's fixed cost is worth 64 KB of loads
+  a.min_units = NDC >= 8 ? 1 : NDC >= 4 ? 2 : 4;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(lsa::paged::NTHREADS);
+  cfg.dynamicSmemBytes = LY::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // no more CTAs than the largest tables could fill
+  const long long most = (static_cast<long long>(a.B) * a.Hkv * a.bt_stride * 2 + a.min_units - 1) / a.min_units;
+  const long long ctas = static_cast<long long>(n_sm) * LY::CTAS_PER_SM;
+  cfg.gridDim = dim3(static_cast<unsigned>(most < ctas ? most : ctas));
+  if (cudaLaunchKernelEx(&cfg, kern, mkv, mq, a) != cudaSuccess) {
+    cudaGetLastError();
+    return LSA_ERR_CUDA;
+  }
+  JoinArgs ja = {};
+  const long long items = static_cast<long long>(a.B) * a.H;
+  // a block for each 128 dims of a head where pairs are split many ways on average, a warp
+  // for each head where most pairs are whole or split in two
+  ja.wide = static_cast<long long>(a.B) * a.Hkv * 4 <= ctas;
+  const int warps = lsa::paged::JOIN_THREADS / 32;
+  ja.out_blocks = static_cast<int>(ja.wide ? items * (a.d / 128) : (items + warps - 1) / warps);
+  long long blocks = ja.out_blocks;
+  if (a.score != nullptr) {
+    // two blocks per SM over the tables, at least one entry per warp
+    const long long total = static_cast<long long>(a.B) * a.bt_stride;
+    long long per = (total + 2 * n_sm - 1) / (2 * n_sm);
+    per = (per + warps - 1) / warps * warps;
+    ja.entries = static_cast<int>(per);
+    ja.chunks = static_cast<int>((a.bt_stride + per - 1) / per);
+    blocks += static_cast<long long>(a.B) * ja.chunks;
+  }
+  const size_t sm_wide = (lsa::paged::MAX_CTAS + 4 * lsa::paged::JOIN_THREADS + 16) * sizeof(float);
+  const size_t sm_warp = static_cast<size_t>(warps) * lsa::paged::MAX_CTAS * sizeof(float);
+  const size_t sm_score = a.score ? (static_cast<size_t>(a.H) + lsa::paged::JOIN_THREADS) * sizeof(float2) : 0;
+  size_t smem = ja.wide ? sm_wide : sm_warp;
+  if (sm_score > smem) smem = sm_score;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(lsa::paged::JOIN_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  if (cudaLaunchKernelEx(&cfg, lsa::paged::paged_join_kernel, a, ja) != cudaSuccess) {
+    cudaGetLastError();
+    return LSA_ERR_CUDA;
+  }
+  return LSA_OK;
+}
+
+template <int HP>
+lsa_status dispatch_d(const CUtensorMap& mkv, const CUtensorMap& mq, const Args& a, int n_sm, cudaStream_t s) {
+  switch (a.d) {
+    case 128: return launch<HP, 2>(mkv, mq, a, n_sm, s);
+    case 256: return launch<HP, 4>(mkv, mq, a, n_sm, s);
+    case 384: return launch<HP, 6>(mkv, mq, a, n_sm, s);
+    default: return launch<HP, 8>(mkv, mq, a, n_sm, s);
+  }
+}
+
+}  // namespace
+
+extern "C" size_t lsa_paged_cache_size(void) { return sizeof(lsa_paged_cache); }
+
+extern "C" size_t lsa_paged_attn_workspace_size(int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                                int32_t bt_stride, int32_t with_score, int32_t n_sm) {
+  if (!valid_shape(B, H, Hkv, d) || bt_stride <= 0 || n_sm <= 0) return 0;
+  return ws_layout(B, H, Hkv, d, bt_stride, with_score != 0, n_sm).bytes;
+}
+
+extern "C" lsa_status lsa_paged_check(const lsa_paged_cache* c) {
+  if (!c || !valid_shape(c->B, c->H, c->Hkv, c->d)) return LSA_ERR_INVALID_ARG;
+  if (c->dtype != LSA_DTYPE_BF16 && c->dtype != LSA_DTYPE_F16) return LSA_ERR_INVALID_ARG;
+  if (c->bt_stride < 1 || c->bt_stride > (1 << 25) || c->free_stride < 0 || c->window < 0)
+    return LSA_ERR_INVALID_ARG;
+  if (!(c->scale > 0.f) || !isfinite(c->scale) || !(c->cap >= 0.f) || !isfinite(c->cap) ||
+      !(c->decay >= 0.f) || !(c->decay <= 1.f))
+    return LSA_ERR_INVALID_ARG;
+  if (!c->pool || (reinterpret_cast<uintptr_t>(c->pool) & 15u) || c->n_pages < 1 ||
+      c->n_pages > (int64_t(1) << 23) / c->Hkv)     // pool rows are int32 coordinates
+    return LSA_ERR_INVALID_ARG;
+  if (!c->t.block_table || !c->t.n_entries || !c->t.tail_len || !c->err) return LSA_ERR_INVALID_ARG;
+  if (c->free_stride > 0 && (!c->t.free_list || !c->t.free_cnt)) return LSA_ERR_INVALID_ARG;
+  return LSA_OK;
+}
+
+extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q, uint16_t* out,
+                                     void* stream) {
+  lsa_host::NvtxRange nvtx_range("lsa_paged_attn");
+  lsa_status st = lsa_paged_check(c);
+  if (st != LSA_OK) return st;
+  if (!q || !out || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u))
+    return LSA_ERR_INVALID_ARG;
+  if (!c->ws || (reinterpret_cast<uintptr_t>(c->ws) & 15u)) return LSA_ERR_INVALID_ARG;
+  const int n_sm = lsa_host::sm_count();
+  if (n_sm <= 0) return LSA_ERR_CUDA;
+  if (2 * n_sm > lsa::paged::MAX_CTAS) return LSA_ERR_UNIMPLEMENTED;
+  const WsLayout w = ws_layout(c->B, c->H, c->Hkv, c->d, c->bt_stride, c->t.score != nullptr, n_sm);
+  if (c->ws_bytes < w.bytes) return LSA_ERR_INVALID_ARG;
+  const int G = c->H / c->Hkv;
+
+  CUtensorMap mkv, mq;
+  st = lsa_host::encode_tiled_2d(&mkv, c->pool, c->d, static_cast<uint64_t>(c->n_pages) * 2 * c->Hkv * LSA_BLOCK,
+                                 static_cast<uint64_t>(c->d) * 2, 64, lsa::paged::UNIT,
+                                 CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != LSA_OK) return st;
+  st = lsa_host::encode_tiled_2d(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H,
+                                 static_cast<uint64_t>(c->d) * 2, 64, G, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != LSA_OK) return st;
+
+  Args a = {};
+  a.block_table = c->t.block_table;
+  a.block_pos = c->t.block_pos;
+  a.n_entries = c->t.n_entries;
+  a.tail_len = c->t.tail_len;
+  a.prefix_len = c->prefix_len;
+  a.doc_start = c->doc_start;
+  a.slopes = c->slopes;
+  a.score = c->t.score;
+  a.out = out;
+  a.err = c->err;
+  uint8_t* ws = static_cast<uint8_t*>(c->ws);
+  a.head = reinterpret_cast<lsa::paged::Head*>(ws + w.head);
+  a.plan = reinterpret_cast<lsa::paged::Plan*>(ws + w.plan);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.unit_w = reinterpret_cast<float2*>(ws + w.unit);
+  a.n_pages = c->n_pages;
+  a.B = c->B;
+  a.H = c->H;
+  a.Hkv = c->Hkv;
+  a.G = G;
+  a.d = c->d;
+  a.bt_stride = c->bt_stride;
+  a.window = c->window;
+  a.f16 = c->dtype == LSA_DTYPE_F16;
+  a.scale = c->scale;
+  a.cap = c->cap;
+  a.decay = c->decay;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (G <= 16) return dispatch_d<16>(mkv, mq, a, n_sm, s);
+  if (G <= 32) return dispatch_d<32>(mkv, mq, a, n_sm, s);
+  return dispatch_d<64>(mkv, mq, a, n_sm, s);
+}

@@ -1,0 +1,424 @@
+// The table side of the paged cache: appending tokens (pages come off a per-sequence stack)
+// and eviction by accumulated attention weight (pages go back on it).
+//
+// Neither computes anything on the values it moves. Append is bound by the bytes of the
+// new rows, eviction by launch and the latency of a few dependent steps: its tables are
+// 12 bytes an entry.
+#include "lsa_common.cuh"
+
+#include <math.h>
+
+namespace lsa {
+namespace paged_tables {
+
+constexpr int PAGE = LSA_BLOCK;
+
+// ------------------------------------------------------------------------ append
+struct AppendArgs {
+  const uint4* k_new;
+  const uint4* v_new;
+  const int32_t* tok_off;     // nullable
+  uint4* pool;
+  lsa_paged_tables src, dst;
+  int32_t* err;
+  long long n_pages, n_tokens;
+  int B, Hkv, row16;          // row16: 16-byte pieces of one head's row (d / 8)
+  int bt_stride, free_stride;
+};
+
+// What one sequence's append does; `grow` pages are taken. bits: error bits, 0 when it goes
+// ahead.
+struct Plan {
+  int n, tail, have, grow, bits;
+  long long off, cnt, held;
+};
+
+__device__ __forceinline__ Plan plan_append(const AppendArgs& a, int b) {
+  Plan p;
+  p.n = a.src.n_entries[b];
+  p.tail = a.src.tail_len[b];
+  p.have = a.free_stride > 0 ? a.src.free_cnt[b] : 0;
+  p.off = a.tok_off ? a.tok_off[b] : b;
+  p.cnt = a.tok_off ? a.tok_off[b + 1] - p.off : 1;
+  p.grow = p.bits = 0;
+  p.held = 0;
+  if (p.n < 0 || p.n > a.bt_stride || (p.n > 0 && (p.tail < 1 || p.tail > PAGE)) || p.have < 0 ||
+      p.have > a.free_stride || p.cnt < 0 || p.off < 0 || p.off + p.cnt > a.n_tokens) {
+    p.bits = LSA_DEVERR_BAD_SIZE;
+    return p;
+  }
+  p.held = p.n > 0 ? static_cast<long long>(p.n - 1) * PAGE + p.tail : 0;
+  const long long grow = (p.held + p.cnt + PAGE - 1) / PAGE - p.n;
+  if (grow > p.have || p.n + grow > a.bt_stride) {
+    p.bits = LSA_DEVERR_POOL_CAPACITY;
+    return p;
+  }
+  p.grow = static_cast<int>(grow);
+  return p;
+}
+
+// Pool row of token i (from 0) of a sequence's new ones, in units of 16 bytes, without the
+// head; -1 for a page outside the pool.
+__device__ __forceinline__ long long token_row(const AppendArgs& a, const Plan& p, int b, long long i) {
+  const long long at = p.held + i;
+  const int e = static_cast<int>(at / PAGE), slot = static_cast<int>(at % PAGE);
+  const int page = e < p.n ? a.src.block_table[static_cast<long long>(b) * a.bt_stride + e]
+                           : a.src.free_list[static_cast<long long>(b) * a.free_stride + p.have - 1 - (e - p.n)];
+  if (page < 0 || page >= a.n_pages) return -1;
+  return (static_cast<long long>(page) * 2 * a.Hkv * PAGE + slot) * a.row16;
+}
+
+// Copy one token's K and V rows: 2 * Hkv * row16 pieces by `step` threads from `first`.
+__device__ __forceinline__ void copy_token(const AppendArgs& a, long long row, long long tok, int first, int step) {
+  const int half = a.Hkv * a.row16;
+  const uint4* ks = a.k_new + tok * half;
+  const uint4* vs = a.v_new + tok * half;
+  const long long head = static_cast<long long>(PAGE) * a.row16;    // pieces from head to head
+  uint4* dst = a.pool + row;
+#pragma unroll 4
+  for (int i = first; i < half; i += step) {
+    const int h = i / a.row16, c = i - h * a.row16;
+    const uint4 k = ks[i], v = vs[i];
+    dst[h * head + c] = k;
+    dst[(a.Hkv + h) * head + c] = v;
+  }
+}
+
+// The tables and counts of sequence b after the append, by `step` threads from `first`. The
+// values it depends on are read before any thread writes (the caller syncs in between).
+__device__ __forceinline__ void write_tables(const AppendArgs& a, const Plan& p, int b, int before, int first, int step) {
+  const long long row = static_cast<long long>(b) * a.bt_stride;
+  for (int g = first; g < p.grow; g += step) {
+    const long long e = row + p.n + g;
+    a.dst.block_table[e] = a.src.free_list[static_cast<long long>(b) * a.free_stride + p.have - 1 - g];
+    if (a.dst.block_pos) a.dst.block_pos[e] = before + 1 + g;
+    if (a.dst.score) a.dst.score[e] = 0.f;
+  }
+  if (first == 0) {
+    const int n = p.n + p.grow;
+    const bool done = p.bits == 0;
+    a.dst.n_entries[b] = n;
+    a.dst.tail_len[b] = done && n > 0 ? static_cast<int>(p.held + p.cnt - static_cast<long long>(n - 1) * PAGE) : p.tail;
+    if (a.free_stride > 0) a.dst.free_cnt[b] = p.have - p.grow;
+    if (!done) set_err(a.err, p.bits);
+  }
+}
+
+// Block position of the last entry (-1 in an empty sequence).
+__device__ __forceinline__ int last_pos(const AppendArgs& a, const Plan& p, int b) {
+  if (p.bits != 0 || p.n == 0) return -1;
+  return a.src.block_pos ? a.src.block_pos[static_cast<long long>(b) * a.bt_stride + p.n - 1] : p.n - 1;
+}
+
+// One token per sequence: a CTA per sequence writes its rows, then its tables.
+__global__ void append_one_kernel(const __grid_constant__ AppendArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.x;
+  const Plan p = plan_append(a, b);
+  const int before = last_pos(a, p, b);
+  if (p.bits == 0) {
+    const long long row = token_row(a, p, b, 0);
+    if (row >= 0)
+      copy_token(a, row, p.off, threadIdx.x, blockDim.x);
+    else if (threadIdx.x == 0)
+      set_err(a.err, LSA_DEVERR_BAD_PAGE);
+  }
+  __syncthreads();                       // every thread has read the counts it needs
+  write_tables(a, p, b, before, threadIdx.x, blockDim.x);
+}
+
+// Ragged appends, rows: a warp per token finds its sequence by bisection of tok_off. The
+// tables are only read here; the next launch writes them.
+__global__ void append_rows_kernel(const __grid_constant__ AppendArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
+  for (long long tok = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; tok < a.n_tokens;
+       tok += warps) {
+    // the last sequence whose offset is <= tok
+    int lo = 0, hi = a.B;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (a.tok_off[mid + 1] <= tok) lo = mid + 1; else hi = mid;
+    }
+    if (lo >= a.B) continue;             // behind the last sequence
+    const Plan p = plan_append(a, lo);
+    if (p.bits != 0 || tok < p.off || tok >= p.off + p.cnt) continue;
+    const long long row = token_row(a, p, lo, tok - p.off);
+    if (row >= 0)
+      copy_token(a, row, tok, lane, 32);
+    else if (lane == 0)
+      set_err(a.err, LSA_DEVERR_BAD_PAGE);
+  }
+}
+
+__global__ void append_tables_kernel(const __grid_constant__ AppendArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.x;
+  const Plan p = plan_append(a, b);
+  const int before = last_pos(a, p, b);
+  __syncthreads();
+  write_tables(a, p, b, before, threadIdx.x, blockDim.x);
+}
+
+// ------------------------------------------------------------------------ eviction
+struct EvictArgs {
+  lsa_paged_tables src, dst;
+  int32_t* err;
+  int bt_stride, free_stride, budget, n_sink, n_recent;
+};
+
+// Order-preserving key of a score: larger scores have larger keys, -0 equals 0, NaN is below all.
+__device__ __forceinline__ uint32_t score_key(float s) {
+  if (s != s) return 0u;
+  const uint32_t u = __float_as_uint(s + 0.f);           // -0 + 0 = 0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct EvictShared {
+  int cnt[2][32];
+  int cnt2[32];
+};
+
+// Sum of v over the block; one barrier, alternating buffers.
+__device__ __forceinline__ int block_sum(int v, EvictShared* s, int which, int warp, int lane, int nwarps) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if (lane == 0) s->cnt[which][warp] = v;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, lane < nwarps ? s->cnt[which][lane] : 0);
+}
+
+// A CTA per sequence. The threshold, the (budget - sink - recent)-th largest key of the middle
+// entries, is found bit by bit from the top: the largest T such that at least that many keys
+// are >= T, one count of the block per bit. Keys stay in registers up to PER per thread;
+// longer rows read them again. Then chunks of blockDim entries are placed in order: kept
+// entries to the front, freed pages onto the stack. A chunk is read whole before any of it
+// is written, and entries only move towards the front, so dst may be src.
+constexpr int PER = 16;
+
+__global__ void __launch_bounds__(1024) evict_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ EvictShared sh;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nt = blockDim.x, nwarps = nt >> 5;
+  const long long row = static_cast<long long>(b) * a.bt_stride;
+  const int32_t* table = a.src.block_table + row;
+  const int32_t* bpos = a.src.block_pos ? a.src.block_pos + row : nullptr;
+  const float* score = a.src.score + row;
+  int32_t* o_table = a.dst.block_table + row;
+  int32_t* o_pos = a.dst.block_pos ? a.dst.block_pos + row : nullptr;
+  float* o_score = a.dst.score + row;
+  const int n = a.src.n_entries[b];
+  const int have = a.src.free_cnt[b];
+  const int tail = a.src.tail_len[b];
+  __syncthreads();                          // the counts are read before any thread writes them
+  int bits = 0;
+  if (n < 0 || n > a.bt_stride || have < 0 || have > a.free_stride) bits = LSA_DEVERR_BAD_SIZE;
+  int gone = bits == 0 && n > a.budget ? n - a.budget : 0;
+  if (gone > 0 && gone > a.free_stride - have) {
+    bits = LSA_DEVERR_POOL_CAPACITY;
+    gone = 0;
+  }
+  if (tid == 0) {
+    a.dst.n_entries[b] = n - gone;
+    a.dst.free_cnt[b] = have + gone;
+    a.dst.tail_len[b] = tail;
+    if (bits) set_err(a.err, bits);
+  }
+  if (bits == LSA_DEVERR_BAD_SIZE) return;
+  if (gone == 0) {
+    if (a.dst.block_table != a.src.block_table)
+      for (int i = tid; i < n; i += nt) o_table[i] = table[i];
+    if (o_pos && a.dst.block_pos != a.src.block_pos)
+      for (int i = tid; i < n; i += nt) o_pos[i] = bpos[i];
+    if (a.dst.score != a.src.score)
+      for (int i = tid; i < n; i += nt) o_score[i] = score[i];
+    return;
+  }
+  const int m0 = a.n_sink, m1 = n - a.n_recent;          // the middle entries
+  const int want = a.budget - a.n_sink - a.n_recent;     // of them are kept: 0 <= want < m1 - m0
+  uint32_t T = 0xffffffffu;                              // keys above T stay,
+  int ties = 0;                                          //   and the first `ties` of those equal to it
+  if (want > 0) {
+    uint32_t key[PER];
+    const bool in_regs = m1 - m0 <= PER * nt;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = m0 + tid + i * nt;
+      key[i] = in_regs && e < m1 ? score_key(score[e]) : 0u;
+    }
+    T = 0u;
+    int which = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t cand = T | (1u << bit);
+      int c = 0;
+      if (in_regs) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c += key[i] >= cand;   // cand >= 1: the padding 0 never counts
+      } else {
+        for (int e = m0 + tid; e < m1; e += nt) c += score_key(score[e]) >= cand;
+      }
+      c = block_sum(c, &sh, which, warp, lane, nwarps);
+      which ^= 1;
+      if (c >= want) T = cand;
+    }
+    int above = 0;
+    if (in_regs) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) above += key[i] > T;
+    } else {
+      for (int e = m0 + tid; e < m1; e += nt) above += score_key(score[e]) > T;
+    }
+    above = block_sum(above, &sh, which, warp, lane, nwarps);
+    ties = want - above;
+  }
+  // placement, a chunk of nt entries at a time
+  int32_t* push = a.dst.free_list + static_cast<long long>(b) * a.free_stride + have;
+  int kept = 0, tied = 0;                                // so far, in earlier chunks
+  for (int c0 = 0; c0 < n; c0 += nt) {
+    const int e = c0 + tid;
+    const bool live = e < n;
+    const int page = live ? table[e] : 0;
+    const int pos = live && bpos ? bpos[e] : 0;
+    const float sc = live ? score[e] : 0.f;
+    const bool mid = live && e >= m0 && e < m1;
+    const uint32_t k = mid && want > 0 ? score_key(sc) : 0u;
+    const bool tie = mid && want > 0 && k == T;
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned tmask = __ballot_sync(0xffffffffu, tie);
+    __syncthreads();                                     // cnt is free, and the last chunk is written
+    if (lane == 0) sh.cnt[0][warp] = __popc(tmask);
+    __syncthreads();
+    const int tw = lane < nwarps ? sh.cnt[0][lane] : 0;
+    const int t_before = __reduce_add_sync(0xffffffffu, lane < warp ? tw : 0);
+    const int t_all = __reduce_add_sync(0xffffffffu, tw);
+    const bool keep = live && (!mid || (want > 0 && (k > T || (tie && tied + t_before + __popc(tmask & below) < ties))));
+    const unsigned kmask = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) sh.cnt2[warp] = __popc(kmask);
+    __syncthreads();                                     // also: every entry of the chunk is read
+    const int kw = lane < nwarps ? sh.cnt2[lane] : 0;
+    const int k_before = __reduce_add_sync(0xffffffffu, lane < warp ? kw : 0);
+    const int to = kept + k_before + __popc(kmask & below);
+    if (keep) {
+      o_table[to] = page;
+      if (o_pos) o_pos[to] = pos;
+      o_score[to] = sc;
+    } else if (live) {
+      push[e - to] = page;                               // entries freed before this one
+    }
+    kept += __reduce_add_sync(0xffffffffu, kw);
+    tied += t_all;
+  }
+}
+
+}  // namespace paged_tables
+}  // namespace lsa
+
+// ------------------------------------------------------------------------ host side
+namespace {
+
+using lsa::paged_tables::AppendArgs;
+using lsa::paged_tables::EvictArgs;
+
+template <typename Args>
+lsa_status launch(void (*kern)(Args), const Args& a, unsigned grid, unsigned block, void* stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+    cudaGetLastError();
+    return LSA_ERR_CUDA;
+  }
+  return LSA_OK;
+}
+
+// dst's arrays: all that the call writes must be there; block_pos and score exactly where
+// the cache has them.
+bool valid_dst(const lsa_paged_cache* c, const lsa_paged_tables& d) {
+  if (!d.block_table || !d.n_entries || !d.tail_len) return false;
+  if ((d.block_pos != nullptr) != (c->t.block_pos != nullptr)) return false;
+  if ((d.score != nullptr) != (c->t.score != nullptr)) return false;
+  return c->free_stride == 0 || (d.free_list && d.free_cnt);
+}
+
+}  // namespace
+
+extern "C" lsa_status lsa_paged_append(const lsa_paged_cache* c, const uint16_t* k_new, const uint16_t* v_new,
+                                       int64_t n_tokens, const int32_t* tok_off, const lsa_paged_tables* dst,
+                                       void* stream) {
+  lsa_host::NvtxRange nvtx_range("lsa_paged_append");
+  const lsa_status st = lsa_paged_check(c);
+  if (st != LSA_OK) return st;
+  const lsa_paged_tables& d = dst ? *dst : c->t;
+  if (!valid_dst(c, d) || n_tokens < 0 || n_tokens > INT32_MAX || (!tok_off && n_tokens != c->B))
+    return LSA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!k_new || !v_new)) return LSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15u) return LSA_ERR_INVALID_ARG;
+  AppendArgs a = {};
+  a.k_new = reinterpret_cast<const uint4*>(k_new);
+  a.v_new = reinterpret_cast<const uint4*>(v_new);
+  a.tok_off = tok_off;
+  a.pool = reinterpret_cast<uint4*>(c->pool);
+  a.src = c->t;
+  a.dst = d;
+  a.err = c->err;
+  a.n_pages = c->n_pages;
+  a.n_tokens = n_tokens;
+  a.B = c->B;
+  a.Hkv = c->Hkv;
+  a.row16 = c->d / 8;
+  a.bt_stride = c->bt_stride;
+  a.free_stride = c->free_stride;
+  const unsigned B = static_cast<unsigned>(c->B);
+  if (!tok_off) {
+    // a thread per 16-byte piece of K, up to 256
+    const int pieces = c->Hkv * a.row16;
+    const unsigned threads = pieces >= 256 ? 256 : pieces >= 128 ? 128 : pieces >= 64 ? 64 : 32;
+    return launch(lsa::paged_tables::append_one_kernel, a, B, threads, stream);
+  }
+  if (n_tokens > 0) {
+    const int n_sm = lsa_host::sm_count();
+    if (n_sm <= 0) return LSA_ERR_CUDA;
+    const int64_t blocks = (n_tokens + 7) / 8;           // 8 warps, a token each
+    const int64_t most = static_cast<int64_t>(n_sm) * 8;
+    const lsa_status s = launch(lsa::paged_tables::append_rows_kernel, a,
+                                static_cast<unsigned>(blocks < most ? blocks : most), 256, stream);
+    if (s != LSA_OK) return s;
+  }
+  return launch(lsa::paged_tables::append_tables_kernel, a, B, 64, stream);
+}
+
+extern "C" lsa_status lsa_paged_evict(const lsa_paged_cache* c, int32_t budget, int32_t n_sink, int32_t n_recent,
+                                      const lsa_paged_tables* dst, void* stream) {
+  lsa_host::NvtxRange nvtx_range("lsa_paged_evict");
+  const lsa_status st = lsa_paged_check(c);
+  if (st != LSA_OK) return st;
+  const lsa_paged_tables& d = dst ? *dst : c->t;
+  if (!valid_dst(c, d) || !c->t.score || c->free_stride < 1) return LSA_ERR_INVALID_ARG;
+  if (budget < 1 || n_sink < 0 || n_recent < 1 || static_cast<int64_t>(n_sink) + n_recent > budget)
+    return LSA_ERR_INVALID_ARG;
+  if (!c->t.block_pos && (c->window > 0 || c->slopes || c->prefix_len || c->doc_start)) return LSA_ERR_INVALID_ARG;
+  EvictArgs a = {};
+  a.src = c->t;
+  a.dst = d;
+  a.err = c->err;
+  a.bt_stride = c->bt_stride;
+  a.free_stride = c->free_stride;
+  a.budget = budget;
+  a.n_sink = n_sink;
+  a.n_recent = n_recent;
+  // up to 4 entries a thread while that keeps the block small: barriers cost more than loads
+  const int want = (c->bt_stride + 3) / 4;
+  const unsigned threads = want > 512 ? 1024 : want > 256 ? 512 : want > 128 ? 256 : want > 64 ? 128 : want > 32 ? 64 : 32;
+  return launch(lsa::paged_tables::evict_kernel, a, static_cast<unsigned>(c->B), threads, stream);
+}
