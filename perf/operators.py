@@ -216,7 +216,7 @@ def prepare(case, seed):
         import lookahead_sparse_kv_lsa_b200 as lsa
         tables = ("block_table", "block_pos", "score", "n_entries", "tail_len", "free_list", "free_cnt")
         s["cache"] = lsa.LsaPagedCache(s["pool"], lsa.LsaPagedTables(**{k: s.get(k) for k in tables}),
-                                       H=c.get("H", 1), scale=s.get("scale", 1.0), cap=c.get("cap", 0.0),
+                                       H=c.get("H", c.get("Hkv", 1)), scale=s.get("scale", 1.0), cap=c.get("cap", 0.0),
                                        window=c.get("window", 0), decay=DECAY, slopes=s.get("slopes"),
                                        prefix_len=s.get("prefix_len"), doc_start=s.get("doc_start"))
         if "dst" in s:
