@@ -219,7 +219,8 @@ template <int HP>
 struct Misc {
   uint64_t full[8], empty[8];
   uint64_t s_full[2], s_free[2];
-  uint64_t p_full, pv_done, q_full, q_free, clean, mma_done;
+  uint64_t p_full, pv_done, q_full, q_free, mma_done;
+  uint64_t clean[4];               // per pair of V stages of a tile
   uint32_t tmem_base;
   int abort;
   int nrec, more, ctas;
@@ -229,6 +230,7 @@ struct Misc {
   int y[YRING];
   float red[4][HP];
   __align__(16) float m[HP];       // running max per head (log2 units), 0 while nothing was seen
+  __align__(16) float over[HP];    // running max + RESCALE_LOG2, -inf while nothing was seen
   __align__(16) float alpha[HP];
   __align__(16) float slope[HP];   // slope * log2 e
   float m_raw[HP];                 // running max, -inf while nothing was seen
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     mbar_init(&m->pv_done, 1);
     mbar_init(&m->q_full, 1);
     mbar_init(&m->q_free, 1);
-    mbar_init(&m->clean, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&m->clean[i], 4);
     mbar_init(&m->mma_done, 1);
     m->abort = 0;
     fence_barrier_init();
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
   int seg_count = 0;     // segments started by this role
   int gtile_s = 0;       // S tiles issued / read
   int gtile_o = 0;       // PV tiles issued / P tiles written
-  int n_clean = 0;       // V stage pairs cleared so far
+  int n_clean = 0;       // tiles with rows to clear so far (MMA)
   for (int batch = 0;; ++batch) {
     const int nrec = m->nrec;
     if (warp == 0) {
@@ -614,10 +616,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                 tc_fence_after();
                 for (int db = 0; db < NDB; ++db) {
                   const int st0 = ring_pos % NST;   // even: the pair (st0, st0 + 1) is adjacent
-                  if (dirty) {
-                    ok = mbar_wait(&m->clean, n_clean & 1, abort);
-                    ++n_clean;
-                  }
+                  if (dirty) ok = mbar_wait(&m->clean[db], n_clean & 1, abort);
                   if (!ok || !mbar_wait(&m->full[st0], (ring_pos / NST) & 1, abort) ||
                       !mbar_wait(&m->full[st0 + 1], (ring_pos / NST) & 1, abort)) {
                     ok = false;
@@ -636,6 +635,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                   ring_pos += 2;
                 }
                 if (!ok) break;
+                if (dirty) ++n_clean;
                 umma_commit(&m->pv_done);
                 ++gtile_o;
               }
@@ -670,6 +670,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           if (t128 < HP) {
             m->m[t128] = 0.f;
             m->m_raw[t128] = -INFINITY;
+            m->over[t128] = -INFINITY;
             m->slope[t128] = a.slopes != nullptr && t128 < G ? a.slopes[h0 + t128] * LOG2E : 0.f;
           }
           float l[HL];
@@ -737,15 +738,10 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
 #pragma unroll
                 for (int h = 0; h < HP; ++h) x[h] = seen ? x[h] : -INFINITY;
               }
-              if (j == 0) {
-                over = true;             // the segment's first tile sets the running max
-              } else {
 #pragma unroll
-                for (int h = 0; h < HP; h += 4) {
-                  const float4 mm = *reinterpret_cast<const float4*>(m->m + h);
-                  over |= x[h] > mm.x + RESCALE_LOG2 || x[h + 1] > mm.y + RESCALE_LOG2 ||
-                          x[h + 2] > mm.z + RESCALE_LOG2 || x[h + 3] > mm.w + RESCALE_LOG2;
-                }
+              for (int h = 0; h < HP; h += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(m->over + h);
+                over |= x[h] > t.x || x[h + 1] > t.y || x[h + 2] > t.z || x[h + 3] > t.w;
               }
             }
             ++gtile_s;
@@ -767,11 +763,11 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                 const float top = fmaxf(fmaxf(m->red[0][h], m->red[1][h]), fmaxf(m->red[2][h], m->red[3][h]));
                 const float old = m->m_raw[h];
                 float al = 1.f;
-                // an unset max (-inf) takes any score; sums kept so far were then all 0
-                if (top > old + RESCALE_LOG2 || (old == -INFINITY && top > old)) {
+                if (top > m->over[h]) {    // an unset max takes any score: the sums so far are 0
                   al = exp2f(old - top);
                   m->m_raw[h] = top;
                   m->m[h] = top;
+                  m->over[h] = top + RESCALE_LOG2;
                 }
                 m->alpha[h] = al;
               }
@@ -842,7 +838,9 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             if (dirty) {
               // Clear the rows that are not seen in each pair of V stages as it arrives. A wait on
               // a stage's phase is sound only when the phase before it is complete: the next
-              // tile's K stages come before this V in the ring, so their product is awaited.
+              // tile's K stages come before this V in the ring, so their product is awaited. Each
+              // pair has a barrier of its own: the warps may run ahead of the product by a whole
+              // tile's pairs, and a wait sees only one phase.
               if (j + 1 < T)
                 failed = !__all_sync(0xffffffffu, mbar_wait(&m->s_full[gtile_s & 1], (gtile_s >> 1) & 1, abort));
               int pos = ring_pos + (j + 1 < T ? (2 * j + 2) * NDC : (2 * T - 1) * NDC);
@@ -862,7 +860,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                 failed = !__all_sync(0xffffffffu, got);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && !failed) mbar_arrive(&m->clean);
+                if (lane == 0 && !failed) mbar_arrive(&m->clean[db]);
               }
             }
           }

@@ -16,13 +16,9 @@ def seen_positions(block_pos, n, tail, prefix=0, doc_start=0, window=0):
     low = doc_start
     if window > 0:
         low = max(low, x_b - window + 1)
-    out = []
-    for j in range(n):
-        for t in range(tail if j == n - 1 else PAGE):
-            x = PAGE * int(block_pos[j]) + t
-            if x < prefix or x >= low:
-                out.append((j, t, x))
-    return out, x_b
+    slots = [(j, t) for j in range(n) for t in range(tail if j == n - 1 else PAGE)]
+    at = [(j, t, PAGE * int(block_pos[j]) + t) for j, t in slots]
+    return [p for p in at if p[2] < prefix or p[2] >= low], x_b
 
 
 def attend(q, pool, table, block_pos, n, tail, scale, cap=0.0, slopes=None, prefix=0, doc_start=0,
@@ -47,8 +43,9 @@ def attend(q, pool, table, block_pos, n, tail, scale, cap=0.0, slopes=None, pref
     at = np.array([p[2] for p in pos], dtype=np.float64)
     page = np.asarray(table)[ent]
     for h in range(H):
-        K = pool[page, 0, h // G, slot]
-        V = pool[page, 1, h // G, slot]
+        if h % G == 0:
+            K, V = pool[page, 0, h // G, slot], pool[page, 1, h // G, slot]
+            aK, aV = np.abs(K), np.abs(V)
         z = scale * (K @ q[h])
         if cap > 0:
             z = cap * np.tanh(z / cap)
@@ -57,8 +54,8 @@ def attend(q, pool, table, block_pos, n, tail, scale, cap=0.0, slopes=None, pref
         w = np.exp(z - z.max())
         w = w / w.sum()
         out[h] = w @ V
-        absv[h] = w @ np.abs(V)
-        big[h] = scale * (np.abs(K) @ np.abs(q[h])).max()
+        absv[h] = w @ aV
+        big[h] = scale * (aK @ np.abs(q[h])).max()
         mass += np.bincount(ent, weights=w, minlength=n)
     return out, mass, absv, big
 

@@ -185,6 +185,43 @@ def test_many_records_per_cta(cuda_ok):
     Case(lens, 1, 1, 128, seed=5).run().check(seqs=[0, 1, 2, 16, 17, 33, 150, 299, 300])
 
 
+LONG = [
+    # lens, H, Hkv, d, dtype, options: many tiles per segment, segments that end anywhere
+    ([1000 + 37 * i for i in range(16)], 32, 8, 128, "fp16", dict(cap=30.0, window=700, prefix=[100 + i for i in range(16)])),
+    ([2500 - 91 * i for i in range(12)], 64, 8, 128, "bf16", dict(docs=[150 * i for i in range(12)], gap=2)),
+    ([9001, 30, 12345, 640], 64, 1, 512, "bf16", dict(cap=50.0)),
+    ([20017], 64, 1, 512, "fp16", dict(window=15001, prefix=[700], gap=2)),
+    ([30011], 20, 1, 512, "bf16", dict(window=20000)),
+    ([8003, 16001], 32, 2, 384, "fp16", dict(prefix=[1000, 33], docs=[4001, 9000])),
+    ([60001, 5], 16, 1, 256, "bf16", dict(window=50001)),
+    ([31000, 200], 33, 1, 256, "bf16", dict(docs=[17, 100])),
+    ([50021], 64, 2, 128, "fp16", dict(prefix=[5000], window=40000)),
+    ([100003], 4, 1, 128, "bf16", dict(slopes=[1.0, 0.1, 0.001, 0.0])),
+    ([60001], 8, 1, 128, "bf16", dict(q_scale=6.0)),
+]
+
+
+@pytest.mark.parametrize("lens,H,Hkv,d,dtype,kw", LONG, ids=[str(c[0][0]) for c in LONG])
+def test_many_tiles_per_cta(cuda_ok, lens, H, Hkv, d, dtype, kw):
+    c = Case(lens, H, Hkv, d, dtype, seed=H, **kw)
+    c.run().check(seqs=range(0, len(lens), 1 if len(lens) < 5 else 5))
+    first = c.out.clone()
+    for _ in range(3):
+        c.run()
+        assert torch.equal(c.out, first)
+    assert c.cache.read_err() == 0
+
+
+@pytest.mark.parametrize("H,d", [(8, 128), (64, 512), (24, 256)])
+def test_a_bad_page_hides_a_whole_tile(cuda_ok, H, d):
+    # the newest units of a segment show nothing, the older ones set its running max
+    c = Case([70000], H, 1, d, seed=14)
+    c.table[0, ::3] = -1
+    c.table[0, 1::3] = 1 << 24
+    c.tables.block_table.copy_(i32(c.table))
+    c.run().check(err=_lib.DEVERR_BAD_PAGE)
+
+
 MASKS = [
     dict(window=1), dict(window=64), dict(window=65), dict(window=200), dict(window=10 ** 6),
     dict(prefix=[1, 63, 64, 65]), dict(prefix=[1, 63, 64, 65], window=1),
