@@ -14,9 +14,10 @@
 //
 // Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
 // e2 on (document, window); they are cut into 32-token units, the same for each key head.
-// The units of all (sequence, key head) pairs, in order, are divided evenly over the CTAs;
-// each (CTA, pair) piece is a segment that leaves (O, max, sum) in the workspace slot
-// CTA + pair, and the joining kernel, a programmatic dependent launch, merges the slots of
+// Every pair (sequence, key head) with anything to see costs its units plus a fixed overhead
+// (filling and draining the pipeline), and the costs of all pairs, in order, are divided
+// evenly over the CTAs; each (CTA, pair) piece is a segment that leaves (O, max, sum) in the
+// workspace slot CTA + pair, and the joining kernel, a programmatic dependent launch, merges the slots of
 // a pair. Nothing waits for another CTA and no counter outlives a call, so a workspace
 // carries no state.
 //
@@ -57,26 +58,32 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int JOIN_THREADS = 256;
 constexpr int MAX_CTAS = 512;
 
-// One sequence, as the attention CTAs and the joining kernel see it.
+// One sequence, as an attention CTA sees it.
 struct Rec {
-  long long base;    // first unit of its first key head in the batch-wide order
   long long ref;     // last position of its last seen entry (origin of the bias)
   long long low;     // positions >= low are seen,
   int pre;           //   and those < pre
   int b, units;      // units of one key head; 0: nothing seen
+  int base;          // cost position of its first key head in the batch-wide order
   int n, tail;       // entries, tokens in the last one
   int e1, e2;        // seen entries: [0, e1) and [e2, n)
   int masked;        // whether low / pre exclude any position of a seen entry
 };
 
+// The split: `total` cost units over `ctas` CTAs, the first `rem` of them with quot + 1.
+struct Split {
+  int total, ctas, quot, rem;
+  __device__ __forceinline__ int start(int cta) const { return cta * quot + min(cta, rem); }
+  // CTA that holds cost position x
+  __device__ __forceinline__ int holder(int x) const {
+    const int big = rem * (quot + 1);
+    return x < big ? x / (quot + 1) : rem + (x - big) / quot;
+  }
+};
+
 // What the joining kernel needs of a sequence (workspace, written by CTA 0).
 struct Plan {
-  long long base;
-  int units, n, e1, e2, tail, pad;
-};
-struct Head {
-  long long U;
-  int ctas, pad;
+  int base, units, n, e1, e2, tail, pad0, pad1;
 };
 
 struct Args {
@@ -90,79 +97,78 @@ struct Args {
   float* score;
   uint16_t* out;
   int32_t* err;
-  Head* head;        // workspace
+  Split* split;      // workspace
   Plan* plan;        // [B]
   float2* part_ml;   // [slot][G] running max (log2 units) and sum
   float* part_o;     // [slot][G][d]
   float2* unit_w;    // [B][bt_stride][2][H] unit sums and the max they refer to
   long long n_pages;
-  int B, H, Hkv, G, d, bt_stride, window, f16, min_units;
+  int B, H, Hkv, G, d, bt_stride, window, f16;
+  int min_cost;      // least cost worth a CTA
+  int overhead;      // cost of a segment besides its units
   float scale, cap, decay;
 };
 
-// First entry whose block position is at least `x` (n if none). Positions ascend strictly, so
-// a run of consecutive blocks at either end answers without a search: the bounds' own
-// entries are looked at first. Whatever the table holds, the answer lies in [0, n].
-__device__ __forceinline__ int first_at_least(const int32_t* pos, int n, long long x) {
-  if (n <= 0) return 0;
-  if (pos == nullptr) return static_cast<int>(x <= 0 ? 0 : x < n ? x : n);
-  const long long first = pos[0], last = pos[n - 1];
+// First entry whose block position is at least `x` (n if none); first and last are the
+// positions of entries 0 and n - 1. Positions ascend strictly, so a run of consecutive blocks
+// at either end answers without a search: the bounds' own entries are looked at first.
+// Whatever the table holds, the answer lies in [0, n].
+__device__ __forceinline__ int first_at_least(const int32_t* pos, int n, long long first, long long last,
+                                              long long x) {
   if (x <= first) return 0;
   if (x > last) return n;
-  long long lo = n - 1 - (last - x), hi = x - first;   // the answer lies in [lo, hi]
-  lo = lo < 0 ? 0 : lo;
-  hi = hi > n - 1 ? n - 1 : hi;
-  if (hi < lo) return static_cast<int>(lo);            // only where positions do not ascend
-  const bool at_lo = pos[lo] >= x;
-  const bool at_hi = hi > 0 && pos[hi - 1] < x;
-  if (at_lo) return static_cast<int>(lo);
-  if (at_hi) return static_cast<int>(hi);
+  if (pos == nullptr) return static_cast<int>(x);
+  const long long lo_ = n - 1 - (last - x), hi_ = x - first;   // the answer lies in [lo, hi]
+  int lo = static_cast<int>(lo_ < 0 ? 0 : lo_), hi = static_cast<int>(hi_ > n - 1 ? n - 1 : hi_);
+  if (hi < lo) return lo;                                // only where positions do not ascend
+  const int at_lo = pos[lo], below_hi = hi > 0 ? pos[hi - 1] : pos[0];
+  if (at_lo >= x) return lo;
+  if (below_hi < x) return hi;
   while (lo < hi) {
-    const long long mid = (lo + hi) >> 1;
+    const int mid = (lo + hi) >> 1;
     if (pos[mid] >= x) hi = mid; else lo = mid + 1;
   }
-  return static_cast<int>(lo);
+  return lo;
 }
 
-__device__ __forceinline__ bool malformed(const Args& a, int b) {
-  const int n = a.n_entries[b];
-  if (n == 0) return false;
-  const int t = a.tail_len[b];
-  return n < 0 || n > a.bt_stride || t < 1 || t > PAGE;
-}
-
-__device__ __forceinline__ Rec read_seq(const Args& a, int b) {
+// Everything that depends on one sequence. The four per-sequence words are loaded together,
+// then (only where a mask or a bias needs them) the positions of the row's ends.
+__device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
   Rec r;
+  const int n = a.n_entries[b];
+  const int tail = a.tail_len[b];
+  const int pre = a.prefix_len ? a.prefix_len[b] : 0;
+  const int doc = a.doc_start ? a.doc_start[b] : 0;
   r.b = b;
   r.base = 0;
   r.ref = 0;
   r.low = 0;
   r.pre = 0;
   r.units = r.n = r.tail = r.e1 = r.e2 = r.masked = 0;
-  const int n = a.n_entries[b];
-  if (n == 0 || malformed(a, b)) return r;
+  bad = n != 0 && (n < 0 || n > a.bt_stride || tail < 1 || tail > PAGE);
+  if (n == 0 || bad) return r;
   r.n = n;
-  r.tail = a.tail_len[b];
-  const int32_t* pos = a.block_pos ? a.block_pos + static_cast<long long>(b) * a.bt_stride : nullptr;
-  const long long last = pos ? pos[n - 1] : n - 1;
-  const long long x_b = last * PAGE + r.tail - 1;
-  long long low = a.doc_start ? a.doc_start[b] : 0;
-  if (a.window > 0 && x_b - a.window + 1 > low) low = x_b - a.window + 1;
-  const int pre = a.prefix_len ? a.prefix_len[b] : 0;
-  if (low > pre && low > 0) {
-    r.masked = 1;
-    r.low = low;
-    r.pre = pre < 0 ? 0 : pre;
-    r.e2 = first_at_least(pos, n, low >> 6);              // its last position >= low
-    r.e1 = first_at_least(pos, n, (static_cast<long long>(r.pre) + PAGE - 1) >> 6);
-    if (r.e1 > r.e2) r.e1 = r.e2;                         // one entry holds both bounds
+  r.tail = tail;
+  const bool masks = doc > 0 || a.window > 0;
+  if (masks || a.slopes != nullptr) {
+    const int32_t* pos = a.block_pos ? a.block_pos + static_cast<long long>(b) * a.bt_stride : nullptr;
+    const long long first = pos ? pos[0] : 0, last = pos ? pos[n - 1] : n - 1;
+    long long low = doc;
+    const long long x_w = last * PAGE + tail - a.window;      // first position of the window
+    if (a.window > 0 && x_w > low) low = x_w;
+    if (low > pre && low > 0) {
+      r.masked = 1;
+      r.low = low;
+      r.pre = pre < 0 ? 0 : pre;
+      r.e2 = first_at_least(pos, n, first, last, low >> 6);   // its last position >= low
+      if (r.pre > 0) r.e1 = first_at_least(pos, n, first, last, (static_cast<long long>(r.pre) + PAGE - 1) >> 6);
+      if (r.e1 > r.e2) r.e1 = r.e2;                           // one entry holds both bounds
+    }
+    const int j = r.e2 < n ? n - 1 : r.e1 - 1;                // last seen entry
+    r.ref = (j == n - 1 || !pos ? (pos ? last : j) : pos[j < 0 ? 0 : j]) * static_cast<long long>(PAGE) + PAGE - 1;
   }
   const int seen = r.e1 + n - r.e2;
-  if (seen > 0) {
-    const int j = r.e2 < n ? n - 1 : r.e1 - 1;            // last seen entry
-    r.ref = (pos ? static_cast<long long>(pos[j]) : j) * PAGE + PAGE - 1;
-    r.units = 2 * seen - (j == n - 1 && r.tail <= UNIT ? 1 : 0);
-  }
+  if (seen > 0) r.units = 2 * seen - ((r.e2 < n || r.e1 == n) && tail <= UNIT ? 1 : 0);
   return r;
 }
 
@@ -177,23 +183,28 @@ struct Seg {
   int kvh, u0, u1;
 };
 
-// Walks the segments of a record inside the CTA's units [us, ue); every role walks the same.
+// Walks the segments of a record inside the CTA's cost range [cs, ce); every role walks the
+// same. A key head's range starts with its overhead, then come its units.
 struct SegWalk {
-  long long cur, end;
-  __device__ __forceinline__ void start(const Rec& r, long long us, long long ue, int Hkv) {
-    cur = us > r.base ? us : r.base;
-    const long long e = r.base + static_cast<long long>(Hkv) * r.units;
-    end = ue < e ? ue : e;
+  int kvh, end, at;       // next key head, heads, cost position of its first unit
+  int cs, ce, step;
+  __device__ __forceinline__ void start(const Rec& r, int cs_, int ce_, const Args& a) {
+    cs = cs_;
+    ce = ce_;
+    step = r.units + a.overhead;
+    kvh = cs > r.base ? (cs - r.base) / step : 0;
+    end = a.Hkv;
+    at = r.base + kvh * step + a.overhead;
   }
   __device__ __forceinline__ bool next(const Rec& r, Seg& s) {
-    if (cur >= end) return false;
-    const long long rel = cur - r.base;
-    s.kvh = static_cast<int>(rel / r.units);
-    s.u0 = static_cast<int>(rel - static_cast<long long>(s.kvh) * r.units);
-    const long long left = end - cur;
-    s.u1 = left < r.units - s.u0 ? s.u0 + static_cast<int>(left) : r.units;
-    cur += s.u1 - s.u0;
-    return true;
+    while (kvh < end && at < ce) {
+      s.kvh = kvh++;
+      s.u0 = max(0, cs - at);
+      s.u1 = min(r.units, ce - at);
+      at += step;
+      if (s.u1 > s.u0) return true;
+    }
+    return false;
   }
 };
 
@@ -223,9 +234,8 @@ struct Misc {
   uint64_t clean[4];               // per pair of V stages of a tile
   uint32_t tmem_base;
   int abort;
-  int nrec, more, ctas;
-  long long U;
-  long long wsum[NTHREADS / 32];
+  int nrec, more, rank0, rank1;
+  unsigned long long wsum[NTHREADS / 32];
   Rec rec[MAXREC];
   int y[YRING];
   float red[4][HP];
@@ -236,23 +246,24 @@ struct Misc {
   float m_raw[HP];                 // running max, -inf while nothing was seen
 };
 
-// Exclusive prefix over the CTA's threads; *total receives the sum.
+// Exclusive prefix over the CTA's threads of two counts in one word; *total receives the sums.
 template <int HP>
-__device__ __forceinline__ long long block_scan(long long v, Misc<HP>* m, int tid, long long* total) {
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, Misc<HP>* m, int tid,
+                                                         unsigned long long* total) {
   const int lane = tid & 31, warp = tid >> 5;
-  long long incl = v;
+  unsigned long long incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
   __syncthreads();
   if (lane == 31) m->wsum[warp] = incl;
   __syncthreads();
-  long long before = 0, sum = 0;
+  unsigned long long before = 0, sum = 0;
 #pragma unroll
   for (int w = 0; w < NTHREADS / 32; ++w) {
-    const long long t = m->wsum[w];
+    const unsigned long long t = m->wsum[w];
     if (w < warp) before += t;
     sum += t;
   }
@@ -260,80 +271,88 @@ __device__ __forceinline__ long long block_scan(long long v, Misc<HP>* m, int ti
   return before + incl - v;
 }
 
-// All threads: the batch's units, this CTA's range of them, and the records that meet it,
+// All threads: the batch's cost, this CTA's range [cs, ce) of it, and the records that meet it,
 // without the first `skip`. CTA 0 also writes the plan for the joining kernel (skip 0).
 template <int HP>
-__device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int tid, long long& us,
-                                      long long& ue) {
-  const bool one = a.B <= NTHREADS;       // one sequence per thread: read it once
+__device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int tid, int& cs, int& ce) {
+  constexpr unsigned long long RANK = 1ull << 32;     // high word: sequences with any cost
+  const bool one = a.B <= NTHREADS;                   // one sequence per thread: read it once
   Rec r;
+  bool bad = false;
   r.units = 0;
-  long long base0 = 0, units = 0;
+  unsigned long long pre = 0, total = 0;
   if (one) {
-    if (tid < a.B) r = read_seq(a, tid);
-    base0 = block_scan(static_cast<long long>(r.units), m, tid, &units);
+    if (tid < a.B) r = read_seq(a, tid, bad);
+    pre = block_scan(r.units > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.units + a.overhead)) : 0ull, m, tid, &total);
   } else {
-    for (int b0 = 0; b0 < a.B; b0 += NTHREADS)
-      if (b0 + tid < a.B) units += read_seq(a, b0 + tid).units;
-    long long total;
-    block_scan(units, m, tid, &total);
-    units = total;
+    unsigned long long mine = 0;
+    for (int b = tid; b < a.B; b += NTHREADS) {
+      const int units = read_seq(a, b, bad).units;
+      if (units > 0) mine += static_cast<unsigned>(a.Hkv * (units + a.overhead));
+    }
+    block_scan(mine, m, tid, &total);
   }
-  const long long U = units * a.Hkv;
-  long long want = (U + a.min_units - 1) / a.min_units;
-  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
-  us = ue = 0;
-  if (static_cast<int>(blockIdx.x) < ctas) {
-    us = (static_cast<long long>(blockIdx.x) * U) / ctas;
-    ue = (static_cast<long long>(blockIdx.x + 1) * U) / ctas;
+  Split sp;
+  sp.total = static_cast<int>(total & 0xffffffffu);
+  sp.ctas = min(static_cast<int>(gridDim.x), (sp.total + a.min_cost - 1) / a.min_cost);
+  sp.quot = sp.ctas > 0 ? sp.total / sp.ctas : 0;
+  sp.rem = sp.total - sp.quot * sp.ctas;
+  const int cta = blockIdx.x;
+  cs = ce = 0;
+  if (cta < sp.ctas) {
+    cs = sp.start(cta);
+    ce = sp.start(cta + 1);
   }
-  const bool write = blockIdx.x == 0 && skip == 0;
-  if (write && tid == 0) {
-    a.head->U = U;
-    a.head->ctas = ctas;
-  }
-  long long found = 0, base = 0;
+  const bool write = cta == 0 && skip == 0;
+  if (write && tid == 0) *a.split = sp;
+  if (tid == 0) m->rank0 = m->rank1 = 0;              // (a CTA without any range)
+  unsigned long long base = 0;
   for (int b0 = 0; b0 < a.B; b0 += NTHREADS) {
     const int b = b0 + tid;
-    long long ex = base0, total = units;
     if (!one) {
       r.units = 0;
-      if (b < a.B) r = read_seq(a, b);
-      ex = block_scan(static_cast<long long>(r.units), m, tid, &total);
+      bad = false;
+      if (b < a.B) r = read_seq(a, b, bad);
+      pre = block_scan(r.units > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.units + a.overhead)) : 0ull, m, tid, &total);
     }
-    const long long first = (base + ex) * a.Hkv;
+    pre += base;
     base += total;
-    if (b < a.B) {
-      r.base = first;
-      if (write) {
-        if (malformed(a, b)) set_err(a.err, LSA_DEVERR_BAD_SIZE);
-        Plan p;
-        p.base = first;
-        p.units = r.units;
-        p.n = r.n;
-        p.e1 = r.e1;
-        p.e2 = r.e2;
-        p.tail = r.tail;
-        p.pad = 0;
-        a.plan[b] = p;
-      }
+    const int first = static_cast<int>(pre & 0xffffffffu), rank = static_cast<int>(pre >> 32);
+    const int behind = first + a.Hkv * (r.units + a.overhead);
+    const bool live = b < a.B && r.units > 0;
+    r.base = first;
+    if (write && b < a.B) {
+      if (bad) set_err(a.err, LSA_DEVERR_BAD_SIZE);
+      Plan p;
+      p.base = first;
+      p.units = r.units;
+      p.n = r.n;
+      p.e1 = r.e1;
+      p.e2 = r.e2;
+      p.tail = r.tail;
+      p.pad0 = p.pad1 = 0;
+      a.plan[b] = p;
     }
-    const bool hit = b < a.B && r.units > 0 && first < ue &&
-                     first + static_cast<long long>(a.Hkv) * r.units > us;
-    long long hits;
-    const long long idx = found + block_scan(hit ? 1ll : 0ll, m, tid, &hits) - skip;
+    const bool hit = live && first < ce && behind > cs;
+    __syncthreads();
+    if (hit && first <= cs) m->rank0 = rank;          // the record that holds cs
+    if (hit && behind >= ce) m->rank1 = rank + 1;
+    __syncthreads();
+    const int idx = rank - m->rank0 - skip;
     if (hit && idx >= 0 && idx < MAXREC) m->rec[idx] = r;
-    found += hits;
   }
+  __syncthreads();
   if (tid == 0) {
-    const long long left = found - skip;
-    m->nrec = static_cast<int>(left > MAXREC ? MAXREC : left < 0 ? 0 : left);
+    const int left = m->rank1 - m->rank0 - skip;
+    m->nrec = left > MAXREC ? MAXREC : left;
     m->more = left > MAXREC;
-    m->ctas = ctas;
-    m->U = U;
   }
   __syncthreads();
 }
+
+// Fixed cost of a segment in units of 32 tokens: 3 to 4 us of pipeline fill and drain, at the
+// 0.75 us (d = 128, two CTAs per SM) to 1.5 us (d = 512) that a unit takes to load.
+__host__ __device__ constexpr int overhead_units(int d) { return d >= 384 ? 2 : d >= 256 ? 3 : 4; }
 
 // Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
 // stage count is even. Up to 32 heads two CTAs share an SM (at most 113 KB each), so that one
@@ -461,8 +480,8 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
   // written before this point.
   grid_dependency_wait();
   grid_dependents_launch();
-  long long us, ue;
-  plan_cta<HP>(a, 0, m, tid, us, ue);      // ends with a block-wide barrier
+  int cs, ce;
+  plan_cta<HP>(a, 0, m, tid, cs, ce);      // ends with a block-wide barrier
   tc_fence_after();
   const uint32_t tmem = m->tmem_base;
 
@@ -484,7 +503,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
         const int32_t* bt = a.block_table + static_cast<long long>(r.b) * a.bt_stride;
         SegWalk walk;
         Seg sg;
-        walk.start(r, us, ue, a.Hkv);
+        walk.start(r, cs, ce, a);
         while (ok && walk.next(r, sg)) {
           const int T = seg_tiles(sg), len = sg.u1 - sg.u0;
           if (lane == 0) {
@@ -567,7 +586,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           const Rec& r = m->rec[ri];
           SegWalk walk;
           Seg sg;
-          walk.start(r, us, ue, a.Hkv);
+          walk.start(r, cs, ce, a);
           while (ok && walk.next(r, sg)) {
             const int T = seg_tiles(sg);
             ok = mbar_wait(&m->q_full, seg_count & 1, abort);
@@ -660,10 +679,12 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
       for (int ri = 0; ri < nrec && !failed; ++ri) {
         const Rec& r = m->rec[ri];
         const int32_t* bt = a.block_table + static_cast<long long>(r.b) * a.bt_stride;
-        const int32_t* bp = a.block_pos ? a.block_pos + static_cast<long long>(r.b) * a.bt_stride : nullptr;
+        // positions are looked up only where a mask or a bias needs them
+        const int32_t* bp = a.block_pos && (r.masked || a.slopes)
+                                ? a.block_pos + static_cast<long long>(r.b) * a.bt_stride : nullptr;
         SegWalk walk;
         Seg sg;
-        walk.start(r, us, ue, a.Hkv);
+        walk.start(r, cs, ce, a);
         while (!failed && walk.next(r, sg)) {
           const int T = seg_tiles(sg);
           const int h0 = sg.kvh * G;
@@ -919,7 +940,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     tc_fence_after();
     if (!m->more || *abort) break;
     __syncthreads();
-    plan_cta<HP>(a, (batch + 1) * MAXREC, m, tid, us, ue);
+    plan_cta<HP>(a, (batch + 1) * MAXREC, m, tid, cs, ce);
   }
   // ---------------------------------------------------------------- teardown
   if (*abort) {
@@ -943,36 +964,36 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
 }
 
 // ------------------------------------------------------------------------ joining
-// CTA holding unit u of the split: the largest c with floor(c * U / ctas) <= u.
-__device__ __forceinline__ int cta_of_unit(long long u, long long U, long long ctas) {
-  return static_cast<int>(((u + 1) * ctas - 1) / U);
-}
-
 struct JoinArgs {
   int out_blocks;    // blocks that join outputs; the rest add the pages' weights
-  int wide;          // a block per (sequence, head, 128 dims); else a warp per (sequence, head)
+  int wide;          // a block per (sequence, head, 128 dims); else a warp
   int entries;       // table entries per block of the second kind
   int chunks;        //   and such blocks per sequence
 };
 
-// out[b][h][cols] = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the n parts of a head,
-// by `groups` groups of threads that take every groups-th part; each thread holds 4 dims.
-__device__ __forceinline__ float4 join_parts(const float* part, const float* w, int n, int first, int step,
-                                             long long stride) {
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = first; k < n; k += step) {
-    const float4 v = *reinterpret_cast<const float4*>(part + k * stride);
-    const float wk = w[k];
-    // a part of weight 0 saw nothing: its values are dropped whatever they are
-    if (wk != 0.f) {
-      acc.x = fmaf(wk, v.x, acc.x);
-      acc.y = fmaf(wk, v.y, acc.y);
-      acc.z = fmaf(wk, v.z, acc.z);
-      acc.w = fmaf(wk, v.w, acc.w);
-    }
+constexpr int JOIN_WARPS = JOIN_THREADS / 32;
+constexpr int WARP_PARTS = 32;   // weights a warp keeps in its lanes at a time
+
+// Parts of head h of sequence b: their number (0: nothing seen) and the first one's slot.
+__device__ __forceinline__ int parts_of(const Args& a, const Split& sp, const Plan& p, int b, int kvh, long long& slot) {
+  if (p.units <= 0) return 0;
+  const int at = p.base + kvh * (p.units + a.overhead) + a.overhead;
+  const int c0 = sp.holder(at), c1 = sp.holder(at + p.units - 1);
+  slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
+  return c1 - c0 + 1;
+}
+
+// A part that saw nothing has weight 0 (its max is -inf), and its values are dropped whatever
+// they are.
+__device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
+
+__device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) {
+  if (w != 0.f) {
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
-  return acc;
 }
 
 __device__ __forceinline__ void store_out(uint16_t* p, float4 v, float inv, bool f16) {
@@ -982,6 +1003,11 @@ __device__ __forceinline__ void store_out(uint16_t* p, float4 v, float inv, bool
   *reinterpret_cast<uint2*>(p) = w;
 }
 
+// out[b][h] = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the parts of a head. A warp or a
+// block takes 128 dims of one head, 4 per lane, so a part is one 512-byte read of a warp.
+//
+// The pages' weights are unit sums relative to the max at the time: score = decay * score +
+// sum over heads of (unit sum) 2^(m_unit - M_h) / L_h.
 __global__ void __launch_bounds__(JOIN_THREADS)
     paged_join_kernel(const __grid_constant__ Args a, const __grid_constant__ JoinArgs ja) {
   extern __shared__ float sm[];
@@ -990,122 +1016,113 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   const bool f16 = a.f16 != 0;
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long U = a.head->U;
-  const long long ctas = a.head->ctas;
+  const Split sp = *a.split;
   if (static_cast<int>(blockIdx.x) < ja.out_blocks) {
-    if (ja.wide) {
-      // -------- a block per (sequence, head, 128 dims): parts split over 8 groups of 32 threads
-      const int chunks = a.d / 128;
-      const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
-      const int b = item / a.H, h = item - b * a.H;
-      const Plan p = a.plan[b];
-      uint16_t* out = a.out + (static_cast<long long>(b) * a.H + h) * a.d + chunk * 128 + lane * 4;
-      const int kvh = h / G;
-      int n = 0, c0 = 0;
-      if (p.units > 0) {
-        const long long v0 = p.base + static_cast<long long>(kvh) * p.units;
-        c0 = cta_of_unit(v0, U, ctas);
-        n = cta_of_unit(v0 + p.units - 1, U, ctas) - c0 + 1;
-      }
-      if (n == 1) return;                       // written by the CTA that held it whole
-      if (n == 0) {
-        if (warp == 0) store_out(out, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, f16);
-        return;
-      }
-      const long long slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
-      const float2* ml = a.part_ml + slot * G + (h - kvh * G);
-      float* w = sm;                            // [n]
-      float4* acc_s = reinterpret_cast<float4*>(sm + MAX_CTAS);
-      float* red = sm + MAX_CTAS + 4 * JOIN_THREADS;
-      float mx = -INFINITY;
-      float2 mine[MAX_CTAS / JOIN_THREADS];
-#pragma unroll
-      for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
-        const int k = tid + i * JOIN_THREADS;
-        mine[i] = k < n ? ml[static_cast<long long>(k) * G] : make_float2(-INFINITY, 0.f);
-        mx = fmaxf(mx, mine[i].x);
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) red[warp] = mx;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < JOIN_THREADS / 32; ++i) mx = fmaxf(mx, red[i]);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
-        const int k = tid + i * JOIN_THREADS;
-        const float wk = mine[i].x == -INFINITY ? 0.f : exp2f(mine[i].x - mx);
-        if (k < n) w[k] = wk;
-        sum += wk == 0.f ? 0.f : wk * mine[i].y;
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) red[8 + warp] = sum;
-      __syncthreads();
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < JOIN_THREADS / 32; ++i) sum += red[8 + i];
-      const float* part = a.part_o + (slot * G + (h - kvh * G)) * a.d + chunk * 128 + lane * 4;
-      acc_s[tid] = join_parts(part, w, n, warp, JOIN_THREADS / 32, static_cast<long long>(G) * a.d);
-      __syncthreads();
-      if (warp == 0) {
-        float4 t = acc_s[lane];
-#pragma unroll
-        for (int i = 1; i < JOIN_THREADS / 32; ++i) {
-          const float4 v = acc_s[i * 32 + lane];
-          t.x += v.x;
-          t.y += v.y;
-          t.z += v.z;
-          t.w += v.w;
-        }
-        store_out(out, t, sum == 0.f ? 0.f : 1.f / sum, f16);
-      }
-      return;
-    }
-    // -------- a warp per (sequence, head)
-    const long long item = static_cast<long long>(blockIdx.x) * (JOIN_THREADS / 32) + warp;
-    if (item >= static_cast<long long>(a.B) * a.H) return;
-    const int b = static_cast<int>(item / a.H), h = static_cast<int>(item - static_cast<long long>(b) * a.H);
-    const Plan p = a.plan[b];
-    uint16_t* out = a.out + item * a.d;
-    const int kvh = h / G;
-    int n = 0, c0 = 0;
-    if (p.units > 0) {
-      const long long v0 = p.base + static_cast<long long>(kvh) * p.units;
-      c0 = cta_of_unit(v0, U, ctas);
-      n = cta_of_unit(v0 + p.units - 1, U, ctas) - c0 + 1;
-    }
-    if (n == 1) return;
-    if (n == 0) {
-      for (int c = lane * 4; c < a.d; c += 128) store_out(out + c, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, f16);
-      return;
-    }
-    const long long slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
+    const int chunks = a.d / 128;
+    const int unit = ja.wide ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
+    const int item = unit / chunks, chunk = unit - item * chunks;
+    const int b = item / a.H, h = item - b * a.H, kvh = h / G;
+    if (b >= a.B) return;
+    long long slot = 0;
+    const int n = parts_of(a, sp, a.plan[b], b, kvh, slot);
+    if (n == 1) return;                         // written by the CTA that held the pair whole
+    uint16_t* out = a.out + static_cast<long long>(item) * a.d + chunk * 128 + lane * 4;
+    const long long stride = static_cast<long long>(G) * a.d;
     const float2* ml = a.part_ml + slot * G + (h - kvh * G);
-    float* w = sm + warp * MAX_CTAS;
-    float mx = -INFINITY;
-    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, ml[static_cast<long long>(k) * G].x);
+    const float* part = a.part_o + slot * stride + (h - kvh * G) * a.d + chunk * 128 + lane * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!ja.wide) {
+      // -------- a warp: the running max over rounds of 32 parts, lane k holding part k's weight
+      float top = -INFINITY, sum = 0.f;
+      for (int k0 = 0; k0 < n; k0 += WARP_PARTS) {
+        const int left = min(WARP_PARTS, n - k0);
+        const float2 mine = lane < left ? ml[static_cast<long long>(k0 + lane) * G] : make_float2(-INFINITY, 0.f);
+        float t = mine.x;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int o = 16; o >= 1; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        t = fmaxf(t, top);
+        const float old = part_weight(top, t);
+        top = t;
+        const float w = part_weight(mine.x, top);
+        float s = w == 0.f ? 0.f : w * mine.y;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        sum = sum * old + s;
+        acc.x *= old;
+        acc.y *= old;
+        acc.z *= old;
+        acc.w *= old;
+        for (int k = 0; k < left; k += 8) {
+          float4 v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (k + e < left) v[e] = *reinterpret_cast<const float4*>(part + (k0 + k + e) * stride);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float wk = __shfl_sync(0xffffffffu, w, (k + e) & 31);
+            if (k + e < left) add_part(acc, wk, v[e]);
+          }
+        }
+      }
+      store_out(out, acc, sum == 0.f ? 0.f : 1.f / sum, f16);
+      return;
+    }
+    // -------- a block: every warp takes every 8th part
+    if (n == 0) {
+      if (warp == 0) store_out(out, acc, 0.f, f16);
+      return;
+    }
+    float* w = sm;                              // [n]
+    float4* acc_s = reinterpret_cast<float4*>(sm + MAX_CTAS);
+    float* red = sm + MAX_CTAS + 4 * JOIN_THREADS;
+    float top = -INFINITY;
+    float2 mine[MAX_CTAS / JOIN_THREADS];
+#pragma unroll
+    for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
+      const int k = tid + i * JOIN_THREADS;
+      mine[i] = k < n ? ml[static_cast<long long>(k) * G] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, mine[i].x);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < JOIN_WARPS; ++i) top = fmaxf(top, red[i]);
     float sum = 0.f;
-    for (int k = lane; k < n; k += 32) {
-      const float2 v = ml[static_cast<long long>(k) * G];
-      const float wk = v.x == -INFINITY ? 0.f : exp2f(v.x - mx);
-      w[k] = wk;
-      sum += wk == 0.f ? 0.f : wk * v.y;
+#pragma unroll
+    for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
+      const int k = tid + i * JOIN_THREADS;
+      const float wk = part_weight(mine[i].x, top);
+      if (k < n) w[k] = wk;
+      sum += wk == 0.f ? 0.f : wk * mine[i].y;
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncwarp();
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float* part = a.part_o + (slot * G + (h - kvh * G)) * a.d;
-    for (int c = lane * 4; c < a.d; c += 128)
-      store_out(out + c, join_parts(part + c, w, n, 0, 1, static_cast<long long>(G) * a.d), inv, f16);
+    if (lane == 0) red[JOIN_WARPS + warp] = sum;
+    __syncthreads();
+    for (int k = warp; k < n; k += 8 * JOIN_WARPS) {
+      float4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (k + e * JOIN_WARPS) * stride);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e * JOIN_WARPS < n) add_part(acc, w[k + e * JOIN_WARPS], v[e]);
+    }
+    acc_s[tid] = acc;
+    __syncthreads();
+    if (warp == 0) {
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < JOIN_WARPS; ++i) sum += red[JOIN_WARPS + i];
+#pragma unroll
+      for (int i = 1; i < JOIN_WARPS; ++i) add_part(acc, 1.f, acc_s[i * 32 + lane]);
+      store_out(out, acc, sum == 0.f ? 0.f : 1.f / sum, f16);
+    }
     return;
   }
-  // -------- the pages' weights: score = decay * score + sum over heads of
-  // (unit sum) 2^(m_unit - M_h) / L_h, with M_h, L_h over all parts of the head
+  // -------- the pages' weights
   const int blk = blockIdx.x - ja.out_blocks;
   const int b = blk / ja.chunks, j0 = (blk - b * ja.chunks) * ja.entries;
   const Plan p = a.plan[b];
@@ -1121,17 +1138,24 @@ __global__ void __launch_bounds__(JOIN_THREADS)
       float M = -INFINITY, L = 0.f;
       if (h < a.H && s < per) {
         const int kvh = h / G;
-        const long long v0 = p.base + static_cast<long long>(kvh) * p.units;
-        const int c0 = cta_of_unit(v0, U, ctas);
-        const int n = cta_of_unit(v0 + p.units - 1, U, ctas) - c0 + 1;
-        const float2* ml = a.part_ml + (c0 + static_cast<long long>(b) * a.Hkv + kvh) * G + (h - kvh * G);
-        // two passes: the max first, so that the sum needs no rescaling (the words are in L1)
-#pragma unroll 4
-        for (int k = s; k < n; k += per) M = fmaxf(M, ml[static_cast<long long>(k) * G].x);
-#pragma unroll 4
-        for (int k = s; k < n; k += per) {
-          const float2 v = ml[static_cast<long long>(k) * G];
-          if (v.y != 0.f) L += v.y * exp2f(v.x - M);
+        long long slot = 0;
+        const int n = parts_of(a, sp, p, b, kvh, slot);
+        const float2* ml = a.part_ml + slot * G + (h - kvh * G);
+        for (int k = s; k < n; k += 8 * per) {
+          float2 v[8];
+          float t = M;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = k + e * per < n ? ml[static_cast<long long>(k + e * per) * G] : make_float2(-INFINITY, 0.f);
+            t = fmaxf(t, v[e].x);
+          }
+          L *= part_weight(M, t);
+          M = t;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w = part_weight(v[e].x, M);
+            if (w != 0.f) L = fmaf(w, v[e].y, L);
+          }
         }
       }
       tmp[tid] = make_float2(M, L);
@@ -1142,7 +1166,8 @@ __global__ void __launch_bounds__(JOIN_THREADS)
           L = 0.f;
           for (int i = 0; i < per; ++i) {
             const float2 v = tmp[i * a.H + h];
-            if (v.y != 0.f) L += v.y * exp2f(v.x - M);
+            const float w = part_weight(v.x, M);
+            if (w != 0.f) L = fmaf(w, v.y, L);
           }
         }
         fin[h] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
@@ -1151,8 +1176,9 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     }
   }
   const int j1 = min(p.n, j0 + ja.entries);
-  for (int j = j0 + warp; j < j1; j += JOIN_THREADS / 32) {
+  for (int j = j0 + warp; j < j1; j += JOIN_WARPS) {
     const long long at = static_cast<long long>(b) * a.bt_stride + j;
+    const float before = a.score[at];
     float mass = 0.f;
     if (p.units > 0 && (j < p.e1 || j >= p.e2)) {
       const int halves = j == p.n - 1 && p.tail <= UNIT ? 1 : 2;
@@ -1161,13 +1187,13 @@ __global__ void __launch_bounds__(JOIN_THREADS)
         const float2 f = fin[h];
         const float2 w0 = uw[h];
         const float2 w1 = halves == 2 ? uw[a.H + h] : make_float2(0.f, 0.f);
-        if (w0.x != 0.f) mass += w0.x * exp2f(w0.y - f.x) * f.y;
-        if (w1.x != 0.f) mass += w1.x * exp2f(w1.y - f.x) * f.y;
+        if (w0.x != 0.f) mass += w0.x * ex2_approx(w0.y - f.x) * f.y;
+        if (w1.x != 0.f) mass += w1.x * ex2_approx(w1.y - f.x) * f.y;
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
     }
-    if (lane == 0) a.score[at] = fmaf(a.decay, a.score[at], mass);
+    if (lane == 0) a.score[at] = fmaf(a.decay, before, mass);
   }
 }
 
@@ -1183,7 +1209,7 @@ using lsa::paged::JoinArgs;
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct WsLayout {
-  size_t head, plan, ml, o, unit, bytes;
+  size_t split, plan, ml, o, unit, bytes;
 };
 
 // Slots: one per CTA and one per (sequence, key head) pair.
@@ -1191,7 +1217,7 @@ WsLayout ws_layout(int B, int H, int Hkv, int d, int bt_stride, bool with_score,
   const size_t G = static_cast<size_t>(H) / Hkv;
   const size_t slots = 2 * static_cast<size_t>(n_sm) + static_cast<size_t>(B) * Hkv;
   WsLayout w;
-  w.head = 0;
+  w.split = 0;
   w.plan = 256;
   w.ml = w.plan + up256(static_cast<size_t>(B) * sizeof(lsa::paged::Plan));
   w.o = w.ml + up256(slots * G * sizeof(float2));
@@ -1211,8 +1237,10 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   auto kern = lsa::paged::paged_attn_kernel<HP, NDC>;
   const lsa_status st = lsa_host::ensure_smem_limit(reinterpret_cast<const void*>(kern), LY::SMEM);
   if (st != LSA_OK) return st;
-  // at least this many 32-token units per CTA: a CTA's fixed cost is worth 64 KB of loads
-  a.min_units = NDC >= 8 ? 1 : NDC >= 4 ? 2 : 4;
+  // A segment's fixed cost in units, and the least a CTA is started for, in units besides it.
+  a.overhead = lsa::paged::overhead_units(NDC * 64);
+  const int min_units = NDC >= 8 ? 1 : NDC >= 4 ? 2 : 4;
+  a.min_cost = min_units + a.overhead;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1223,7 +1251,7 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // no more CTAs than the largest tables could fill
-  const long long most = (static_cast<long long>(a.B) * a.Hkv * a.bt_stride * 2 + a.min_units - 1) / a.min_units;
+  const long long most = static_cast<long long>(a.B) * a.Hkv * ((2ll * a.bt_stride + min_units - 1) / min_units);
   const long long ctas = static_cast<long long>(n_sm) * LY::CTAS_PER_SM;
   cfg.gridDim = dim3(static_cast<unsigned>(most < ctas ? most : ctas));
   if (cudaLaunchKernelEx(&cfg, kern, mkv, mq, a) != cudaSuccess) {
@@ -1231,12 +1259,11 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
     return LSA_ERR_CUDA;
   }
   JoinArgs ja = {};
-  const long long items = static_cast<long long>(a.B) * a.H;
-  // a block for each 128 dims of a head where pairs are split many ways on average, a warp
-  // for each head where most pairs are whole or split in two
-  ja.wide = static_cast<long long>(a.B) * a.Hkv * 4 <= ctas;
-  const int warps = lsa::paged::JOIN_THREADS / 32;
-  ja.out_blocks = static_cast<int>(ja.wide ? items * (a.d / 128) : (items + warps - 1) / warps);
+  const long long items = static_cast<long long>(a.B) * a.H * (a.d / 128);
+  // a block for each 128 dims of a head where pairs are split over 24 CTAs or more on average
+  ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
+  const int warps = lsa::paged::JOIN_WARPS;
+  ja.out_blocks = static_cast<int>(ja.wide ? items : (items + warps - 1) / warps);
   long long blocks = ja.out_blocks;
   if (a.score != nullptr) {
     // two blocks per SM over the tables, at least one entry per warp
@@ -1248,9 +1275,8 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
     blocks += static_cast<long long>(a.B) * ja.chunks;
   }
   const size_t sm_wide = (lsa::paged::MAX_CTAS + 4 * lsa::paged::JOIN_THREADS + 16) * sizeof(float);
-  const size_t sm_warp = static_cast<size_t>(warps) * lsa::paged::MAX_CTAS * sizeof(float);
   const size_t sm_score = a.score ? (static_cast<size_t>(a.H) + lsa::paged::JOIN_THREADS) * sizeof(float2) : 0;
-  size_t smem = ja.wide ? sm_wide : sm_warp;
+  size_t smem = ja.wide ? sm_wide : 0;
   if (sm_score > smem) smem = sm_score;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(lsa::paged::JOIN_THREADS);
@@ -1295,6 +1321,9 @@ extern "C" lsa_status lsa_paged_check(const lsa_paged_cache* c) {
     return LSA_ERR_INVALID_ARG;
   if (!c->t.block_table || !c->t.n_entries || !c->t.tail_len || !c->err) return LSA_ERR_INVALID_ARG;
   if (c->free_stride > 0 && (!c->t.free_list || !c->t.free_cnt)) return LSA_ERR_INVALID_ARG;
+  // the attention's cost positions are int32
+  if (static_cast<int64_t>(c->B) * c->Hkv * (2 * static_cast<int64_t>(c->bt_stride) + 4) > (int64_t(1) << 30))
+    return LSA_ERR_INVALID_ARG;
   return LSA_OK;
 }
 
@@ -1334,7 +1363,7 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   a.out = out;
   a.err = c->err;
   uint8_t* ws = static_cast<uint8_t*>(c->ws);
-  a.head = reinterpret_cast<lsa::paged::Head*>(ws + w.head);
+  a.split = reinterpret_cast<lsa::paged::Split*>(ws + w.split);
   a.plan = reinterpret_cast<lsa::paged::Plan*>(ws + w.plan);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
