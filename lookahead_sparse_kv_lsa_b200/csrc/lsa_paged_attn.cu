@@ -13,25 +13,24 @@
 // up to 64 heads, as long as the products run on the tensor cores.
 //
 // Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
-// e2 on (document, window); they are cut into 32-token units, the same for each key head.
-// Every pair (sequence, key head) with anything to see costs its units plus a fixed overhead
-// (filling and draining the pipeline), and the costs of all pairs, in order, are divided
-// evenly over the CTAs; each (CTA, pair) piece is a segment that leaves (O, max, sum) in the
+// e2 on (document, window), the same for each key head. Every pair (sequence, key head) with
+// anything to see costs its pages plus a fixed overhead (filling and draining the pipeline),
+// and the costs of all pairs, in order, are divided evenly over the CTAs; each (CTA, pair) piece is a segment that leaves (O, max, sum) in the
 // workspace slot CTA + pair, and the joining kernel, a programmatic dependent launch, merges the slots of
 // a pair. Nothing waits for another CTA and no counter outlives a call, so a workspace
 // carries no state.
 //
-// Within a segment, tiles of up to 128 tokens run newest first (a bias that falls with the
+// Within a segment, tiles of two pages run newest first (a bias that falls with the
 // distance then sets the running max once), in a pipeline of three roles:
 //   warp 0    reads the page table and issues TMA loads: Q once per segment, K and V tiles
-//             in 16 KB stages of [128 tokens][64 dims] through a ring;
+//             in 16 KB stages of [128 tokens][64 dims], a box a page, through a ring;
 //   warp 1    tcgen05.mma: S^T[token][head] = K Q^T (M = 128, N = heads padded to 16, 32 or
 //             64), double buffered in TMEM; O^T[dim][head] += V^T P (M = 128 dims, K = 128
 //             tokens), accumulated in TMEM;
 //   warps 2-5 softmax, one token row per thread: the row's scores stay in registers from the
 //             one TMEM load to the rounding of P. A vote (one barrier with reduction) finds
 //             whether any score exceeds its head's running max by more than 2^8; only then is
-//             the tile max formed and O^T rescaled. Each unit's per-head sums (a butterfly
+//             the tile max formed and O^T rescaled. Each half page's per-head sums (a butterfly
 //             over the warp's 32 rows) feed the denominators and, where scores are kept, go
 //             to the workspace with the max they refer to.
 // P is written token-major ([128 tokens][heads], 16-byte stores) and read by the tensor cores
@@ -47,12 +46,12 @@ namespace lsa {
 namespace paged {
 
 constexpr int PAGE = LSA_BLOCK;
-constexpr int UNIT = 32;                  // tokens per work unit: the rows of a softmax warp
-constexpr int TILE = 128;                 // tokens per tile: the MMA M of S^T
+constexpr int HALF = 32;                  // rows of a softmax warp: half a page
+constexpr int TILE = 128;                 // tokens per tile, two pages: the MMA M of S^T
 constexpr int STAGE_BYTES = TILE * 128;   // [128 rows][64 dims] 16-bit = 16 KB
 constexpr int NTHREADS = 192;
 constexpr int MAXREC = 16;                // sequences a CTA plans at a time
-constexpr int YRING = 256;                // units whose pool rows the producer has looked up
+constexpr int YRING = 128;                // pages whose pool rows the producer has looked up
 constexpr float RESCALE_LOG2 = 8.0f;      // raise the running max only by more than 2^8
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int JOIN_THREADS = 256;
@@ -63,7 +62,7 @@ struct Rec {
   long long ref;     // last position of its last seen entry (origin of the bias)
   long long low;     // positions >= low are seen,
   int pre;           //   and those < pre
-  int b, units;      // units of one key head; 0: nothing seen
+  int b, pages;      // seen entries; 0: nothing seen
   int base;          // cost position of its first key head in the batch-wide order
   int n, tail;       // entries, tokens in the last one
   int e1, e2;        // seen entries: [0, e1) and [e2, n)
@@ -83,7 +82,7 @@ struct Split {
 
 // What the joining kernel needs of a sequence (workspace, written by CTA 0).
 struct Plan {
-  int base, units, n, e1, e2, tail, pad0, pad1;
+  int base, pages, n, e1, e2, pad0, pad1, pad2;
 };
 
 struct Args {
@@ -101,11 +100,11 @@ struct Args {
   Plan* plan;        // [B]
   float2* part_ml;   // [slot][G] running max (log2 units) and sum
   float* part_o;     // [slot][G][d]
-  float2* unit_w;    // [B][bt_stride][2][H] unit sums and the max they refer to
+  float2* half_w;    // [B][bt_stride][2][H] half pages' sums and the max they refer to
   long long n_pages;
   int B, H, Hkv, G, d, bt_stride, window, f16;
   int min_cost;      // least cost worth a CTA
-  int overhead;      // cost of a segment besides its units
+  int overhead;      // cost of a segment besides its pages
   float scale, cap, decay;
 };
 
@@ -144,7 +143,7 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
   r.ref = 0;
   r.low = 0;
   r.pre = 0;
-  r.units = r.n = r.tail = r.e1 = r.e2 = r.masked = 0;
+  r.pages = r.n = r.tail = r.e1 = r.e2 = r.masked = 0;
   bad = n != 0 && (n < 0 || n > a.bt_stride || tail < 1 || tail > PAGE);
   if (n == 0 || bad) return r;
   r.n = n;
@@ -167,31 +166,27 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
     const int j = r.e2 < n ? n - 1 : r.e1 - 1;                // last seen entry
     r.ref = (j == n - 1 || !pos ? (pos ? last : j) : pos[j < 0 ? 0 : j]) * static_cast<long long>(PAGE) + PAGE - 1;
   }
-  const int seen = r.e1 + n - r.e2;
-  if (seen > 0) r.units = 2 * seen - ((r.e2 < n || r.e1 == n) && tail <= UNIT ? 1 : 0);
+  r.pages = r.e1 + n - r.e2;
   return r;
 }
 
-// Entry of the seen unit u.
-__device__ __forceinline__ int unit_entry(const Rec& r, int u) {
-  const int v = u >> 1;
-  return v < r.e1 ? v : r.e2 + v - r.e1;
-}
+// Entry of the seen page u.
+__device__ __forceinline__ int page_entry(const Rec& r, int u) { return u < r.e1 ? u : r.e2 + u - r.e1; }
 
-// A piece of one (sequence, key head) pair held by one CTA: units [u0, u1).
+// A piece of one (sequence, key head) pair held by one CTA: seen pages [u0, u1).
 struct Seg {
   int kvh, u0, u1;
 };
 
 // Walks the segments of a record inside the CTA's cost range [cs, ce); every role walks the
-// same. A key head's range starts with its overhead, then come its units.
+// same. A key head's range starts with its overhead, then come its pages.
 struct SegWalk {
-  int kvh, end, at;       // next key head, heads, cost position of its first unit
+  int kvh, end, at;       // next key head, heads, cost position of its first page
   int cs, ce, step;
   __device__ __forceinline__ void start(const Rec& r, int cs_, int ce_, const Args& a) {
     cs = cs_;
     ce = ce_;
-    step = r.units + a.overhead;
+    step = r.pages + a.overhead;
     kvh = cs > r.base ? (cs - r.base) / step : 0;
     end = a.Hkv;
     at = r.base + kvh * step + a.overhead;
@@ -200,7 +195,7 @@ struct SegWalk {
     while (kvh < end && at < ce) {
       s.kvh = kvh++;
       s.u0 = max(0, cs - at);
-      s.u1 = min(r.units, ce - at);
+      s.u1 = min(r.pages, ce - at);
       at += step;
       if (s.u1 > s.u0) return true;
     }
@@ -208,22 +203,21 @@ struct SegWalk {
   }
 };
 
-__device__ __forceinline__ int seg_tiles(const Seg& s) { return (s.u1 - s.u0 + 3) >> 2; }
+__device__ __forceinline__ int seg_tiles(const Seg& s) { return (s.u1 - s.u0 + 1) >> 1; }
 
-// Units [t0, t1) of tile t, newest tile first. The partial tile (fewer than 4 units) is
-// tile 0: its small loads overlap the pipeline fill.
-__device__ __forceinline__ void tile_units(const Seg& s, int t, int& t0, int& t1) {
-  const int len = s.u1 - s.u0;
-  const int first = (len & 3) ? (len & 3) : 4;
-  t1 = t == 0 ? s.u1 : s.u1 - first - 4 * (t - 1);
-  t0 = t == 0 ? s.u1 - first : t1 - 4;
+// Pages [t0, t1) of tile t, newest tile first. An odd page out is tile 0: its smaller loads
+// overlap the pipeline fill.
+__device__ __forceinline__ void tile_pages(const Seg& s, int t, int& t0, int& t1) {
+  const int first = 2 - ((s.u1 - s.u0) & 1);
+  t1 = t == 0 ? s.u1 : s.u1 - first - 2 * (t - 1);
+  t0 = t == 0 ? s.u1 - first : t1 - 2;
 }
 
 // Whether a tile may hold rows that are loaded but not seen: the end of the tail page and
 // the entries at the masks' bounds. Every role gives the same answer.
 __device__ __forceinline__ bool tile_dirty(const Rec& r, int t0, int t1) {
-  if (t1 == r.units && (r.tail & (UNIT - 1)) != 0 && (r.e2 < r.n || r.e1 == r.n)) return true;
-  return r.masked && t1 > 2 * (r.e1 - 1) && t0 < 2 * (r.e1 + 1);
+  if (t1 == r.pages && r.tail < PAGE && (r.e2 < r.n || r.e1 == r.n)) return true;
+  return r.masked && t1 > r.e1 - 1 && t0 < r.e1 + 1;
 }
 
 template <int HP>
@@ -279,16 +273,16 @@ __device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int 
   const bool one = a.B <= NTHREADS;                   // one sequence per thread: read it once
   Rec r;
   bool bad = false;
-  r.units = 0;
+  r.pages = 0;
   unsigned long long pre = 0, total = 0;
   if (one) {
     if (tid < a.B) r = read_seq(a, tid, bad);
-    pre = block_scan(r.units > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.units + a.overhead)) : 0ull, m, tid, &total);
+    pre = block_scan(r.pages > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.pages + a.overhead)) : 0ull, m, tid, &total);
   } else {
     unsigned long long mine = 0;
     for (int b = tid; b < a.B; b += NTHREADS) {
-      const int units = read_seq(a, b, bad).units;
-      if (units > 0) mine += static_cast<unsigned>(a.Hkv * (units + a.overhead));
+      const int pages = read_seq(a, b, bad).pages;
+      if (pages > 0) mine += static_cast<unsigned>(a.Hkv * (pages + a.overhead));
     }
     block_scan(mine, m, tid, &total);
   }
@@ -310,27 +304,26 @@ __device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int 
   for (int b0 = 0; b0 < a.B; b0 += NTHREADS) {
     const int b = b0 + tid;
     if (!one) {
-      r.units = 0;
+      r.pages = 0;
       bad = false;
       if (b < a.B) r = read_seq(a, b, bad);
-      pre = block_scan(r.units > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.units + a.overhead)) : 0ull, m, tid, &total);
+      pre = block_scan(r.pages > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.pages + a.overhead)) : 0ull, m, tid, &total);
     }
     pre += base;
     base += total;
     const int first = static_cast<int>(pre & 0xffffffffu), rank = static_cast<int>(pre >> 32);
-    const int behind = first + a.Hkv * (r.units + a.overhead);
-    const bool live = b < a.B && r.units > 0;
+    const int behind = first + a.Hkv * (r.pages + a.overhead);
+    const bool live = b < a.B && r.pages > 0;
     r.base = first;
     if (write && b < a.B) {
       if (bad) set_err(a.err, LSA_DEVERR_BAD_SIZE);
       Plan p;
       p.base = first;
-      p.units = r.units;
+      p.pages = r.pages;
       p.n = r.n;
       p.e1 = r.e1;
       p.e2 = r.e2;
-      p.tail = r.tail;
-      p.pad0 = p.pad1 = 0;
+      p.pad0 = p.pad1 = p.pad2 = 0;
       a.plan[b] = p;
     }
     const bool hit = live && first < ce && behind > cs;
@@ -350,9 +343,9 @@ __device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int 
   __syncthreads();
 }
 
-// Fixed cost of a segment in units of 32 tokens: 3 to 4 us of pipeline fill and drain, at the
-// 0.75 us (d = 128, two CTAs per SM) to 1.5 us (d = 512) that a unit takes to load.
-__host__ __device__ constexpr int overhead_units(int d) { return d >= 384 ? 2 : d >= 256 ? 3 : 4; }
+// Fixed cost of a segment in pages: 3 to 4 us of pipeline fill and drain, at the 1.5 us
+// (d = 128, two CTAs per SM) to 3 us (d = 512) that a page takes to load.
+__host__ __device__ constexpr int overhead_pages(int d) { return d >= 384 ? 1 : 2; }
 
 // Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
 // stage count is even. Up to 32 heads two CTAs share an SM (at most 113 KB each), so that one
@@ -405,16 +398,35 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
   return d;
 }
 
-// tanh(t) * c for the capped scores. tanh t = 1 - 2 / (1 + 2^(2 t log2 e)) is off by a few
-// 2^-24 in absolute terms; where |t| < 1/16 that is much of the result, and the Taylor
-// series t (1 - t^2/3 + 2 t^4/15) is used (relative error below 17/315 t^6 < 4e-9).
-__device__ __forceinline__ float cap_tanh(float t, float c) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(2.f * LOG2E * t)));
-  const float big = fmaf(-2.f, r, 1.f);
-  const float t2 = t * t;
-  const float small = t * fmaf(t2, fmaf(t2, 2.f / 15.f, -1.f / 3.f), 1.f);
-  return c * (fabsf(t) < 0.0625f ? small : big);
+// x = c tanh(k x) for a row of scores, c in log2 units: tanh t = 1 - 2 / (1 + 2^(2 t log2 e)) is
+// off by a few 2^-24 in absolute terms, so a capped score by c times that. Up to SMALL_CAP that
+// is no more than the rounding of a score near the cap; above it small scores would lose, and
+// where |t| < 1/16 the Taylor series t (1 - t^2/3 + 2 t^4/15) is used (relative error below
+// 17/315 t^6 < 4e-9). The special functions of 16 heads are issued together, so that their
+// latencies overlap.
+constexpr float SMALL_CAP = 64.0f * LOG2E;
+template <int HP, bool SERIES>
+__device__ __forceinline__ void cap_scores(float (&x)[HP], float k, float c) {
+  const float k2 = 2.f * LOG2E * k;
+#pragma unroll
+  for (int h = 0; h < HP; h += 16) {
+    float e[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(x[h + i] * k2));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(1.f + e[i]));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float big = fmaf(-2.f * c, e[i], c);
+      if constexpr (SERIES) {
+        const float t = x[h + i] * k, t2 = t * t;
+        const float small = c * t * fmaf(t2, fmaf(t2, 2.f / 15.f, -1.f / 3.f), 1.f);
+        x[h + i] = fabsf(t) < 0.0625f ? small : big;
+      } else {
+        x[h + i] = big;
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
@@ -425,8 +437,21 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
 }
-__device__ __forceinline__ uint16_t to16(float v, bool f16) {
-  return static_cast<uint16_t>(pack16(v, 0.f, f16) & 0xffffu);
+// Lane i of a quad gives (v0, v1, v2, v3) and gets value i of lanes 0 .. 3.
+__device__ __forceinline__ float4 quad_transpose(float v0, float v1, float v2, float v3, int i) {
+  const bool o1 = i & 1, o2 = i & 2;
+  float a = __shfl_xor_sync(0xffffffffu, o1 ? v0 : v1, 1);
+  float b = __shfl_xor_sync(0xffffffffu, o1 ? v2 : v3, 1);
+  if (o1) {
+    v0 = a;
+    v2 = b;
+  } else {
+    v1 = a;
+    v3 = b;
+  }
+  a = __shfl_xor_sync(0xffffffffu, o2 ? v0 : v2, 2);
+  b = __shfl_xor_sync(0xffffffffu, o2 ? v1 : v3, 2);
+  return o2 ? make_float4(a, b, v2, v3) : make_float4(v0, v1, a, b);
 }
 
 template <int HP, int NDC>
@@ -516,24 +541,23 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             }
           }
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          int filled = 0;                 // units of the segment looked up, newest first
+          int filled = 0;                 // pages of the segment looked up, newest first
           for (int i = 0; i <= T && ok; ++i) {
             int t0, t1;
-            tile_units(sg, i, t0, t1);
+            tile_pages(sg, i, t0, t1);
             if (i < T && sg.u1 - t0 > filled) {
-              // the pool rows of the next 128 units, by all lanes
+              // the pool rows of the next 64 pages, by all lanes
               __syncwarp();
 #pragma unroll
               for (int e = 0; e < YRING / 64; ++e) {
                 const int k = filled + 32 * e + lane;
                 if (k < len) {
-                  const int u = sg.u1 - 1 - k;
-                  const int page = bt[unit_entry(r, u)];
+                  const int page = bt[page_entry(r, sg.u1 - 1 - k)];
                   int y = -1;
                   if (page < 0 || page >= a.n_pages)
                     set_err(a.err, LSA_DEVERR_BAD_PAGE);
                   else
-                    y = (page * 2 * a.Hkv + sg.kvh) * PAGE + (u & 1) * UNIT;
+                    y = (page * 2 * a.Hkv + sg.kvh) * PAGE;
                   m->y[k & (YRING - 1)] = y;
                 }
               }
@@ -545,11 +569,11 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                 // stage order per step i: K of tile i, then V of tile i-1
                 const int tile = kv == 0 ? i : i - 1;
                 if (tile < 0 || tile >= T) continue;
-                tile_units(sg, tile, t0, t1);
-                int ys[4];
+                tile_pages(sg, tile, t0, t1);
+                int ys[2];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  // rows past the tile's units and bad pages: a box outside the map, which
+                for (int x = 0; x < 2; ++x) {
+                  // rows past the tile's pages and bad pages: a box outside the map, which
                   // the copy engine fills with zeros without reading memory
                   const int u = t0 + x;
                   const int y = u < t1 ? m->y[(sg.u1 - 1 - u) & (YRING - 1)] : -1;
@@ -562,8 +586,8 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                   mbar_arrive_expect_tx(&m->full[st], STAGE_BYTES);
                   uint8_t* dst = sRing + st * STAGE_BYTES;
 #pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    tma_load_2d_hint(dst + x * (UNIT * 128), &map_kv, &m->full[st], 64 * c, ys[x],
+                  for (int x = 0; x < 2; ++x)
+                    tma_load_2d_hint(dst + x * (PAGE * 128), &map_kv, &m->full[st], 64 * c, ys[x],
                                      evict_first);
                   ++ring_pos;
                 }
@@ -626,7 +650,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
               if (i >= 1) {
                 const int j = i - 1;
                 int t0, t1;
-                tile_units(sg, j, t0, t1);
+                tile_pages(sg, j, t0, t1);
                 const bool dirty = tile_dirty(r, t0, t1);
                 if (!mbar_wait(&m->p_full, gtile_o & 1, abort)) {
                   ok = false;
@@ -666,7 +690,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
       // ---------------------------------------------------------------- softmax
       // Every wait result is folded into the next barrier with reduction, so the four warps
       // leave together and no named barrier is left half-arrived.
-      const int sw = warp & 3;                   // TMEM lanes, and unit of the tile, of this warp
+      const int sw = warp & 3;                   // TMEM lanes, and half page of the tile, of this warp
       const int t128 = tid - 64;
       const uint32_t row = sw * 32 + lane;       // token row of the tile
       const uint32_t lane_addr = static_cast<uint32_t>(sw * 32) << 16;
@@ -697,32 +721,33 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           float l[HL];
 #pragma unroll
           for (int i = 0; i < HL; ++i) l[i] = 0.f;
-          // this warp's unit of the next tile is looked up one tile ahead
+          // this warp's page of the next tile is looked up one tile ahead
           int t0, t1;
-          tile_units(sg, 0, t0, t1);
+          tile_pages(sg, 0, t0, t1);
           int page_n = -1, pos_n = 0;
-          if (t0 + sw < t1) {
-            const int e = unit_entry(r, t0 + sw);
+          if (t0 + (sw >> 1) < t1) {
+            const int e = page_entry(r, t0 + (sw >> 1));
             page_n = bt[e];
             pos_n = bp ? bp[e] : e;
           }
           named_bar_sync(1, 128);
           for (int j = 0; j < T; ++j) {
-            tile_units(sg, j, t0, t1);
+            tile_pages(sg, j, t0, t1);
             const bool dirty = tile_dirty(r, t0, t1);
-            const int u = t0 + sw;
+            const int u = t0 + (sw >> 1);
+            const int in_page = (sw & 1) * HALF + lane;
             const int page = page_n;
-            const long long x0 = static_cast<long long>(pos_n) * PAGE + (u & 1) * UNIT + lane;
+            const long long x0 = static_cast<long long>(pos_n) * PAGE + in_page;
             if (j + 1 < T) {
               int n0, n1;
-              tile_units(sg, j + 1, n0, n1);
-              const int e = unit_entry(r, n0 + sw);      // tiles after the first hold 4 units
+              tile_pages(sg, j + 1, n0, n1);
+              const int e = page_entry(r, n0 + (sw >> 1));   // tiles after the first are whole
               page_n = bt[e];
               pos_n = bp ? bp[e] : e;
             }
             bool seen = u < t1 && page >= 0 && page < a.n_pages;
-            const int entry = u < t1 ? unit_entry(r, u) : 0;
-            if (seen && entry == r.n - 1) seen = (u & 1) * UNIT + lane < r.tail;
+            const int entry = u < t1 ? page_entry(r, u) : 0;
+            if (seen && entry == r.n - 1) seen = in_page < r.tail;
             if (seen && r.masked) seen = x0 < r.pre || x0 >= r.low;
             const bool all_seen = __all_sync(0xffffffffu, seen);
             const int sb = gtile_s & 1;
@@ -738,8 +763,10 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
               __syncwarp();
               if (lane == 0) mbar_arrive(&m->s_free[sb]);
               if (a.cap > 0.f) {
-#pragma unroll
-                for (int h = 0; h < HP; ++h) x[h] = cap_tanh(x[h] * scale2, cap2);
+                if (cap2 <= SMALL_CAP)
+                  cap_scores<HP, false>(x, scale2, cap2);
+                else
+                  cap_scores<HP, true>(x, scale2, cap2);
               } else {
 #pragma unroll
                 for (int h = 0; h < HP; ++h) x[h] *= scale2;
@@ -759,11 +786,16 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
 #pragma unroll
                 for (int h = 0; h < HP; ++h) x[h] = seen ? x[h] : -INFINITY;
               }
+              bool o0 = false, o1 = false, o2 = false, o3 = false;   // four chains of comparisons
 #pragma unroll
               for (int h = 0; h < HP; h += 4) {
                 const float4 t = *reinterpret_cast<const float4*>(m->over + h);
-                over |= x[h] > t.x || x[h + 1] > t.y || x[h + 2] > t.z || x[h + 3] > t.w;
+                o0 |= x[h] > t.x;
+                o1 |= x[h + 1] > t.y;
+                o2 |= x[h + 2] > t.z;
+                o3 |= x[h + 3] > t.w;
               }
+              over = (o0 || o1) || (o2 || o3);
             }
             ++gtile_s;
             // one vote: bit 0 of the barrier's OR says that some wait failed or some score is over
@@ -796,7 +828,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
 #pragma unroll
               for (int i = 0; i < HL; ++i) l[i] *= m->alpha[h_lane + i];
             }
-            // weights; their fp32 sums per unit and head
+            // weights; their fp32 sums per half page and head
             uint32_t pw[HP / 2];
 #pragma unroll
             for (int h = 0; h < HP; h += 4) {
@@ -819,7 +851,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
 #pragma unroll
             for (int i = 0; i < HL; ++i) l[i] += x[i];
             if (a.score != nullptr && u < t1) {
-              float2* uw = a.unit_w + ((static_cast<long long>(r.b) * a.bt_stride + entry) * 2 + (u & 1)) * a.H + h0;
+              float2* uw = a.half_w + ((static_cast<long long>(r.b) * a.bt_stride + entry) * 2 + (sw & 1)) * a.H + h0;
               if (HP >= 32 || (lane & 1) == 0) {
 #pragma unroll
                 for (int i = 0; i < HL; ++i)
@@ -904,7 +936,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           // a pair held whole by this CTA is normalised and written out here; a split one
           // leaves its part in slot CTA + pair. The (max, sum) pairs of both go to the
           // workspace: the pages' weights are normalised by them.
-          const bool whole = sg.u0 == 0 && sg.u1 == r.units;
+          const bool whole = sg.u0 == 0 && sg.u1 == r.pages;
           const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(r.b) * a.Hkv + sg.kvh;
           if (t128 < G) {
             const float sum = m->red[0][t128] + m->red[1][t128] + m->red[2][t128] + m->red[3][t128];
@@ -912,21 +944,37 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             m->alpha[t128] = sum == 0.f ? 0.f : 1.f / sum;
           }
           named_bar_sync(1, 128);
-          uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0) * a.d + row;
-          float* po = a.part_o + slot * G * a.d + row;
+          // Lanes hold one dim of every head. Quads exchange 4 x 4 so that a lane holds 4 dims of
+          // one head: a store of a warp then covers 32 dims of 4 heads, whole 128-byte lines.
+          const int quad = lane >> 2, i4 = lane & 3;
+          uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0 + i4) * a.d + sw * 32 + quad * 4;
+          float* po = a.part_o + (slot * G + i4) * a.d + sw * 32 + quad * 4;
 #pragma unroll 1
-          for (int db = 0; db < NDB; ++db) {
+          for (int db = 0; db < NDB; ++db, fo += 128, po += 128) {
             float o[HP];
             tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
             tmem_wait_ld();
-            if (whole) {
+            // no branch inside the common loop, so that its shuffles overlap
+            if (G == HP && !whole) {
 #pragma unroll
-              for (int h = 0; h < HP; ++h)
-                if (h < G) fo[h * a.d + db * 128] = to16(o[h] * m->alpha[h], f16);
+              for (int h = 0; h < HP; h += 4)
+                *reinterpret_cast<float4*>(po + h * a.d) = quad_transpose(o[h], o[h + 1], o[h + 2], o[h + 3], i4);
             } else {
 #pragma unroll
-              for (int h = 0; h < HP; ++h)
-                if (h < G) po[h * a.d + db * 128] = o[h];
+              for (int h = 0; h < HP; h += 4) {
+                if (h < G) {
+                  const float4 v = quad_transpose(o[h], o[h + 1], o[h + 2], o[h + 3], i4);
+                  if (h + i4 < G) {
+                    if (whole) {
+                      const float inv = m->alpha[h + i4];
+                      *reinterpret_cast<uint2*>(fo + h * a.d) =
+                          make_uint2(pack16(v.x * inv, v.y * inv, f16), pack16(v.z * inv, v.w * inv, f16));
+                    } else {
+                      *reinterpret_cast<float4*>(po + h * a.d) = v;
+                    }
+                  }
+                }
+              }
             }
           }
           tc_fence_before();
@@ -976,9 +1024,9 @@ constexpr int WARP_PARTS = 32;   // weights a warp keeps in its lanes at a time
 
 // Parts of head h of sequence b: their number (0: nothing seen) and the first one's slot.
 __device__ __forceinline__ int parts_of(const Args& a, const Split& sp, const Plan& p, int b, int kvh, long long& slot) {
-  if (p.units <= 0) return 0;
-  const int at = p.base + kvh * (p.units + a.overhead) + a.overhead;
-  const int c0 = sp.holder(at), c1 = sp.holder(at + p.units - 1);
+  if (p.pages <= 0) return 0;
+  const int at = p.base + kvh * (p.pages + a.overhead) + a.overhead;
+  const int c0 = sp.holder(at), c1 = sp.holder(at + p.pages - 1);
   slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
   return c1 - c0 + 1;
 }
@@ -1006,8 +1054,8 @@ __device__ __forceinline__ void store_out(uint16_t* p, float4 v, float inv, bool
 // out[b][h] = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the parts of a head. A warp or a
 // block takes 128 dims of one head, 4 per lane, so a part is one 512-byte read of a warp.
 //
-// The pages' weights are unit sums relative to the max at the time: score = decay * score +
-// sum over heads of (unit sum) 2^(m_unit - M_h) / L_h.
+// The pages' weights are sums over half pages relative to the max at the time: score = decay *
+// score + sum over heads of (sum) 2^(m - M_h) / L_h.
 __global__ void __launch_bounds__(JOIN_THREADS)
     paged_join_kernel(const __grid_constant__ Args a, const __grid_constant__ JoinArgs ja) {
   extern __shared__ float sm[];
@@ -1019,8 +1067,8 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   const Split sp = *a.split;
   if (static_cast<int>(blockIdx.x) < ja.out_blocks) {
     const int chunks = a.d / 128;
-    const int unit = ja.wide ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
-    const int item = unit / chunks, chunk = unit - item * chunks;
+    const int job = ja.wide ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
+    const int item = job / chunks, chunk = job - item * chunks;
     const int b = item / a.H, h = item - b * a.H, kvh = h / G;
     if (b >= a.B) return;
     long long slot = 0;
@@ -1129,7 +1177,7 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   if (j0 >= p.n) return;
   float2* fin = reinterpret_cast<float2*>(sm);                 // [H]: (M, 1 / L)
   float2* tmp = fin + a.H;                                     // [JOIN_THREADS]
-  if (p.units > 0) {
+  if (p.pages > 0) {
     // threads over (part, head), heads fastest: consecutive threads read consecutive words
     const int per = a.H < JOIN_THREADS ? JOIN_THREADS / a.H : 1;   // parts read side by side
     for (int h0 = 0; h0 < a.H; h0 += JOIN_THREADS) {
@@ -1180,13 +1228,12 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     const long long at = static_cast<long long>(b) * a.bt_stride + j;
     const float before = a.score[at];
     float mass = 0.f;
-    if (p.units > 0 && (j < p.e1 || j >= p.e2)) {
-      const int halves = j == p.n - 1 && p.tail <= UNIT ? 1 : 2;
-      const float2* uw = a.unit_w + at * 2 * a.H;
+    if (p.pages > 0 && (j < p.e1 || j >= p.e2)) {
+      const float2* uw = a.half_w + at * 2 * a.H;
       for (int h = lane; h < a.H; h += 32) {
         const float2 f = fin[h];
         const float2 w0 = uw[h];
-        const float2 w1 = halves == 2 ? uw[a.H + h] : make_float2(0.f, 0.f);
+        const float2 w1 = uw[a.H + h];
         if (w0.x != 0.f) mass += w0.x * ex2_approx(w0.y - f.x) * f.y;
         if (w1.x != 0.f) mass += w1.x * ex2_approx(w1.y - f.x) * f.y;
       }
@@ -1209,7 +1256,7 @@ using lsa::paged::JoinArgs;
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct WsLayout {
-  size_t split, plan, ml, o, unit, bytes;
+  size_t split, plan, ml, o, half, bytes;
 };
 
 // Slots: one per CTA and one per (sequence, key head) pair.
@@ -1221,8 +1268,8 @@ WsLayout ws_layout(int B, int H, int Hkv, int d, int bt_stride, bool with_score,
   w.plan = 256;
   w.ml = w.plan + up256(static_cast<size_t>(B) * sizeof(lsa::paged::Plan));
   w.o = w.ml + up256(slots * G * sizeof(float2));
-  w.unit = w.o + up256(slots * G * d * sizeof(float));
-  w.bytes = w.unit + (with_score ? up256(static_cast<size_t>(B) * bt_stride * 2 * H * sizeof(float2)) : 0);
+  w.half = w.o + up256(slots * G * d * sizeof(float));
+  w.bytes = w.half + (with_score ? up256(static_cast<size_t>(B) * bt_stride * 2 * H * sizeof(float2)) : 0);
   return w;
 }
 
@@ -1237,10 +1284,10 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   auto kern = lsa::paged::paged_attn_kernel<HP, NDC>;
   const lsa_status st = lsa_host::ensure_smem_limit(reinterpret_cast<const void*>(kern), LY::SMEM);
   if (st != LSA_OK) return st;
-  // A segment's fixed cost in units, and the least a CTA is started for, in units besides it.
-  a.overhead = lsa::paged::overhead_units(NDC * 64);
-  const int min_units = NDC >= 8 ? 1 : NDC >= 4 ? 2 : 4;
-  a.min_cost = min_units + a.overhead;
+  // A segment's fixed cost in pages, and the least a CTA is started for, in pages besides it.
+  a.overhead = lsa::paged::overhead_pages(NDC * 64);
+  const int min_pages = NDC >= 4 ? 1 : 2;
+  a.min_cost = min_pages + a.overhead;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1251,7 +1298,7 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // no more CTAs than the largest tables could fill
-  const long long most = static_cast<long long>(a.B) * a.Hkv * ((2ll * a.bt_stride + min_units - 1) / min_units);
+  const long long most = static_cast<long long>(a.B) * a.Hkv * ((static_cast<long long>(a.bt_stride) + min_pages - 1) / min_pages);
   const long long ctas = static_cast<long long>(n_sm) * LY::CTAS_PER_SM;
   cfg.gridDim = dim3(static_cast<unsigned>(most < ctas ? most : ctas));
   if (cudaLaunchKernelEx(&cfg, kern, mkv, mq, a) != cudaSuccess) {
@@ -1322,7 +1369,7 @@ extern "C" lsa_status lsa_paged_check(const lsa_paged_cache* c) {
   if (!c->t.block_table || !c->t.n_entries || !c->t.tail_len || !c->err) return LSA_ERR_INVALID_ARG;
   if (c->free_stride > 0 && (!c->t.free_list || !c->t.free_cnt)) return LSA_ERR_INVALID_ARG;
   // the attention's cost positions are int32
-  if (static_cast<int64_t>(c->B) * c->Hkv * (2 * static_cast<int64_t>(c->bt_stride) + 4) > (int64_t(1) << 30))
+  if (static_cast<int64_t>(c->B) * c->Hkv * (static_cast<int64_t>(c->bt_stride) + 2) > (int64_t(1) << 30))
     return LSA_ERR_INVALID_ARG;
   return LSA_OK;
 }
@@ -1344,7 +1391,7 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
 
   CUtensorMap mkv, mq;
   st = lsa_host::encode_tiled_2d(&mkv, c->pool, c->d, static_cast<uint64_t>(c->n_pages) * 2 * c->Hkv * LSA_BLOCK,
-                                 static_cast<uint64_t>(c->d) * 2, 64, lsa::paged::UNIT,
+                                 static_cast<uint64_t>(c->d) * 2, 64, lsa::paged::PAGE,
                                  CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != LSA_OK) return st;
   st = lsa_host::encode_tiled_2d(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H,
@@ -1367,7 +1414,7 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   a.plan = reinterpret_cast<lsa::paged::Plan*>(ws + w.plan);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
-  a.unit_w = reinterpret_cast<float2*>(ws + w.unit);
+  a.half_w = reinterpret_cast<float2*>(ws + w.half);
   a.n_pages = c->n_pages;
   a.B = c->B;
   a.H = c->H;

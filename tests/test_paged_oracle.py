@@ -106,7 +106,7 @@ def _cache(**kw):
 
 BAD = [dict(B=0), dict(B=65537), dict(H=0), dict(H=7), dict(Hkv=0), dict(H=130), dict(H=2048, Hkv=64),
        dict(d=64), dict(d=96), dict(d=640), dict(dtype=2), dict(dtype=-1), dict(bt_stride=0),
-       dict(free_stride=-1), dict(B=65536, bt_stride=1 << 13), dict(bt_stride=(1 << 25) + 1), dict(window=-1), dict(scale=0.0), dict(scale=float("nan")),
+       dict(free_stride=-1), dict(B=65536, bt_stride=1 << 14), dict(bt_stride=(1 << 25) + 1), dict(window=-1), dict(scale=0.0), dict(scale=float("nan")),
        dict(scale=float("inf")), dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")),
        dict(decay=-0.1), dict(decay=1.5), dict(decay=float("nan")), dict(pool=None), dict(pool=8),
        dict(n_pages=0), dict(n_pages=(1 << 22) + 1), dict(block_table=None), dict(n_entries=None),
