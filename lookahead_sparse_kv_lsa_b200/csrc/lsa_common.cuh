@@ -136,6 +136,15 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -409,6 +418,11 @@ lsa_status ensure_smem_limit(const void* func, int bytes);
 lsa_status encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                            uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                            CUtensorMapSwizzle swizzle);
+
+// Map of a 16-bit row-major matrix [rows][d] as [d/64][rows][64]: one copy brings `box_rows`
+// rows as d/64 adjacent tiles of [box_rows][64] with the 128-byte swizzle (coordinates 0, row, 0).
+lsa_status encode_tiled_rows(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows,
+                             uint32_t box_rows);
 
 // Fused token append for the decode-step path: k_new / v_new [B][d] go into slot
 // tail-1 of each sequence's last block-table page; tail_len_out receives `tail`.

@@ -130,6 +130,25 @@ __device__ __forceinline__ int first_at_least(const int32_t* pos, int n, long lo
   return lo;
 }
 
+// Before the grid dependency: nothing may be read yet, but prefetches into L2 are only hints, and
+// they also bring the pages' translations, which cost a first access more than the data.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ void warm_up(const Args& a, int tid) {
+  if (tid < a.B && (tid & 31) == 0) {
+    prefetch_l2(a.n_entries + tid);
+    prefetch_l2(a.tail_len + tid);
+    if (a.prefix_len) prefetch_l2(a.prefix_len + tid);
+    if (a.doc_start) prefetch_l2(a.doc_start + tid);
+  }
+  if (tid == 1) prefetch_l2(a.block_table);
+  if (tid == 2 && a.block_pos) prefetch_l2(a.block_pos);
+  if (tid == 3) prefetch_l2(a.plan);
+  if (tid == 4) prefetch_l2(a.part_o);
+  if (tid == 5 && a.slopes) prefetch_l2(a.slopes);
+}
+
 // Everything that depends on one sequence. The four per-sequence words are loaded together,
 // then (only where a mask or a bias needs them) the positions of the row's ends.
 __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
@@ -494,12 +513,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     tmem_alloc(&m->tmem_base, LY::TMEM_COLS);
     tmem_relinquish();
   }
-  // rows of the padded heads: zeros, so that their scores are 0 and need no masks
-  for (int i = tid; i < NDC * (HP - G) * 8; i += NTHREADS) {
-    const int c = i / ((HP - G) * 8), k = i - c * (HP - G) * 8;
-    *reinterpret_cast<uint4*>(sQ + c * HP * 128 + G * 128 + k * 16) = make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async_smem();
+  warm_up(a, tid);
   tc_fence_before();
   // Launched as a programmatic dependent: nothing a preceding kernel may write is read or
   // written before this point.
@@ -534,9 +548,10 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           if (lane == 0) {
             if (seg_count > 0) ok = mbar_wait(&m->q_free, (seg_count - 1) & 1, abort);
             if (ok) {
-              mbar_arrive_expect_tx(&m->q_full, NDC * G * 128);
-              for (int c = 0; c < NDC; ++c)
-                tma_load_2d(sQ + c * HP * 128, &map_q, &m->q_full, 64 * c, r.b * a.H + sg.kvh * G);
+              // HP rows, of which the rows past the group's G belong to other heads or lie
+              // outside q (zeros): columns that nobody reads
+              mbar_arrive_expect_tx(&m->q_full, LY::Q_BYTES);
+              tma_load_3d(sQ, &map_q, &m->q_full, 0, r.b * a.H + sg.kvh * G, 0);
               ++seg_count;
             }
           }
@@ -1062,6 +1077,10 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.G;
   const bool f16 = a.f16 != 0;
+  if (tid == 0) prefetch_l2(a.split);
+  if (tid == 1) prefetch_l2(a.part_o);
+  if (tid == 2) prefetch_l2(a.out);
+  if (tid == 3 && a.score) prefetch_l2(a.score);
   grid_dependency_wait();
   grid_dependents_launch();
   const Split sp = *a.split;
@@ -1084,6 +1103,10 @@ __global__ void __launch_bounds__(JOIN_THREADS)
       float top = -INFINITY, sum = 0.f;
       for (int k0 = 0; k0 < n; k0 += WARP_PARTS) {
         const int left = min(WARP_PARTS, n - k0);
+        float4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) v[e] = *reinterpret_cast<const float4*>(part + (k0 + e) * stride);
         const float2 mine = lane < left ? ml[static_cast<long long>(k0 + lane) * G] : make_float2(-INFINITY, 0.f);
         float t = mine.x;
 #pragma unroll
@@ -1101,10 +1124,11 @@ __global__ void __launch_bounds__(JOIN_THREADS)
         acc.z *= old;
         acc.w *= old;
         for (int k = 0; k < left; k += 8) {
-          float4 v[8];
+          if (k > 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (k + e < left) v[e] = *reinterpret_cast<const float4*>(part + (k0 + k + e) * stride);
+            for (int e = 0; e < 8; ++e)
+              if (k + e < left) v[e] = *reinterpret_cast<const float4*>(part + (k0 + k + e) * stride);
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float wk = __shfl_sync(0xffffffffu, w, (k + e) & 31);
@@ -1123,6 +1147,10 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     float* w = sm;                              // [n]
     float4* acc_s = reinterpret_cast<float4*>(sm + MAX_CTAS);
     float* red = sm + MAX_CTAS + 4 * JOIN_THREADS;
+    float4 v[10];                               // this warp's first parts, before the weights
+#pragma unroll
+    for (int e = 0; e < 10; ++e)
+      if (warp + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (warp + e * JOIN_WARPS) * stride);
     float top = -INFINITY;
     float2 mine[MAX_CTAS / JOIN_THREADS];
 #pragma unroll
@@ -1149,13 +1177,14 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) red[JOIN_WARPS + warp] = sum;
     __syncthreads();
-    for (int k = warp; k < n; k += 8 * JOIN_WARPS) {
-      float4 v[8];
+    for (int k = warp; k < n; k += 10 * JOIN_WARPS) {
+      if (k > warp) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (k + e * JOIN_WARPS) * stride);
+        for (int e = 0; e < 10; ++e)
+          if (k + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (k + e * JOIN_WARPS) * stride);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 10; ++e)
         if (k + e * JOIN_WARPS < n) add_part(acc, w[k + e * JOIN_WARPS], v[e]);
     }
     acc_s[tid] = acc;
@@ -1189,18 +1218,18 @@ __global__ void __launch_bounds__(JOIN_THREADS)
         long long slot = 0;
         const int n = parts_of(a, sp, p, b, kvh, slot);
         const float2* ml = a.part_ml + slot * G + (h - kvh * G);
-        for (int k = s; k < n; k += 8 * per) {
-          float2 v[8];
+        for (int k = s; k < n; k += 16 * per) {
+          float2 v[16];
           float t = M;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < 16; ++e) {
             v[e] = k + e * per < n ? ml[static_cast<long long>(k + e * per) * G] : make_float2(-INFINITY, 0.f);
             t = fmaxf(t, v[e].x);
           }
           L *= part_weight(M, t);
           M = t;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < 16; ++e) {
             const float w = part_weight(v[e].x, M);
             if (w != 0.f) L = fmaf(w, v[e].y, L);
           }
@@ -1223,24 +1252,34 @@ __global__ void __launch_bounds__(JOIN_THREADS)
       __syncthreads();
     }
   }
+  // a warp takes four entries at a time, so that their loads overlap
   const int j1 = min(p.n, j0 + ja.entries);
-  for (int j = j0 + warp; j < j1; j += JOIN_WARPS) {
+  for (int j = j0 + 4 * warp; j < j1; j += 4 * JOIN_WARPS) {
     const long long at = static_cast<long long>(b) * a.bt_stride + j;
-    const float before = a.score[at];
-    float mass = 0.f;
-    if (p.pages > 0 && (j < p.e1 || j >= p.e2)) {
-      const float2* uw = a.half_w + at * 2 * a.H;
+    const float before = lane < 4 && j + lane < j1 ? a.score[at + lane] : 0.f;
+    float mass[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.pages > 0) {
+      bool live[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) live[e] = j + e < j1 && (j + e < p.e1 || j + e >= p.e2);
+      const float2* hw = a.half_w + at * 2 * a.H;
       for (int h = lane; h < a.H; h += 32) {
+        float2 w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = live[e / 2] ? hw[e * a.H + h] : make_float2(0.f, 0.f);
         const float2 f = fin[h];
-        const float2 w0 = uw[h];
-        const float2 w1 = uw[a.H + h];
-        if (w0.x != 0.f) mass += w0.x * ex2_approx(w0.y - f.x) * f.y;
-        if (w1.x != 0.f) mass += w1.x * ex2_approx(w1.y - f.x) * f.y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (w[e].x != 0.f) mass[e / 2] += w[e].x * ex2_approx(w[e].y - f.x) * f.y;
       }
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      for (int o = 16; o >= 1; o >>= 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mass[e] += __shfl_xor_sync(0xffffffffu, mass[e], o);
+      }
     }
-    if (lane == 0) a.score[at] = fmaf(a.decay, before, mass);
+    const float m = lane == 0 ? mass[0] : lane == 1 ? mass[1] : lane == 2 ? mass[2] : mass[3];
+    if (lane < 4 && j + lane < j1) a.score[at + lane] = fmaf(a.decay, before, m);
   }
 }
 
@@ -1313,10 +1352,10 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   ja.out_blocks = static_cast<int>(ja.wide ? items : (items + warps - 1) / warps);
   long long blocks = ja.out_blocks;
   if (a.score != nullptr) {
-    // two blocks per SM over the tables, at least one entry per warp
+    // two blocks per SM over the tables, at least four entries each
     const long long total = static_cast<long long>(a.B) * a.bt_stride;
     long long per = (total + 2 * n_sm - 1) / (2 * n_sm);
-    per = (per + warps - 1) / warps * warps;
+    per = (per + 3) / 4 * 4;
     ja.entries = static_cast<int>(per);
     ja.chunks = static_cast<int>((a.bt_stride + per - 1) / per);
     blocks += static_cast<long long>(a.B) * ja.chunks;
@@ -1394,8 +1433,8 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
                                  static_cast<uint64_t>(c->d) * 2, 64, lsa::paged::PAGE,
                                  CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != LSA_OK) return st;
-  st = lsa_host::encode_tiled_2d(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H,
-                                 static_cast<uint64_t>(c->d) * 2, 64, G, CU_TENSOR_MAP_SWIZZLE_128B);
+  const int HP = G <= 16 ? 16 : G <= 32 ? 32 : 64;
+  st = lsa_host::encode_tiled_rows(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H, HP);
   if (st != LSA_OK) return st;
 
   Args a = {};
@@ -1428,7 +1467,9 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   a.cap = c->cap;
   a.decay = c->decay;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (G <= 16) return dispatch_d<16>(mkv, mq, a, n_sm, s);
-  if (G <= 32) return dispatch_d<32>(mkv, mq, a, n_sm, s);
-  return dispatch_d<64>(mkv, mq, a, n_sm, s);
+  switch (HP) {
+    case 16: return dispatch_d<16>(mkv, mq, a, n_sm, s);
+    case 32: return dispatch_d<32>(mkv, mq, a, n_sm, s);
+    default: return dispatch_d<64>(mkv, mq, a, n_sm, s);
+  }
 }
