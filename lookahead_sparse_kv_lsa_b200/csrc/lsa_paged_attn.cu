@@ -50,7 +50,7 @@ constexpr int HALF = 32;                  // rows of a softmax warp: half a page
 constexpr int TILE = 128;                 // tokens per tile, two pages: the MMA M of S^T
 constexpr int STAGE_BYTES = TILE * 128;   // [128 rows][64 dims] 16-bit = 16 KB
 constexpr int NTHREADS = 192;
-constexpr int MAXREC = 16;                // sequences a CTA plans at a time
+constexpr int MAXREC = 32;                // sequences a CTA plans at a time
 constexpr int YRING = 128;                // pages whose pool rows the producer has looked up
 constexpr float RESCALE_LOG2 = 8.0f;      // raise the running max only by more than 2^8
 constexpr float LOG2E = 1.4426950408889634f;
@@ -248,7 +248,8 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   int nrec, more, rank0, rank1;
-  unsigned long long wsum[NTHREADS / 32];
+  int cs, ce;                      // the CTA's cost range
+  int2 wsum[NTHREADS / 32];
   Rec rec[MAXREC];
   int y[YRING];
   float red[4][HP];
@@ -259,98 +260,141 @@ struct Misc {
   float m_raw[HP];                 // running max, -inf while nothing was seen
 };
 
-// Exclusive prefix over the CTA's threads of two counts in one word; *total receives the sums.
+// Exclusive prefixes over the CTA's threads of a cost and of a flag; tot receives the sums.
 template <int HP>
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, Misc<HP>* m, int tid,
-                                                         unsigned long long* total) {
+__device__ __forceinline__ int2 block_scan(int cost, bool flag, Misc<HP>* m, int tid, int2& tot) {
   const int lane = tid & 31, warp = tid >> 5;
-  unsigned long long incl = v;
+  int incl = cost;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
+  const unsigned mask = __ballot_sync(0xffffffffu, flag);
   __syncthreads();
-  if (lane == 31) m->wsum[warp] = incl;
+  if (lane == 31) m->wsum[warp] = make_int2(incl, __popc(mask));
   __syncthreads();
-  unsigned long long before = 0, sum = 0;
+  int2 pre = make_int2(incl - cost, __popc(mask & ((1u << lane) - 1u)));
+  tot = make_int2(0, 0);
 #pragma unroll
   for (int w = 0; w < NTHREADS / 32; ++w) {
-    const unsigned long long t = m->wsum[w];
-    if (w < warp) before += t;
-    sum += t;
+    const int2 t = m->wsum[w];
+    if (w < warp) {
+      pre.x += t.x;
+      pre.y += t.y;
+    }
+    tot.x += t.x;
+    tot.y += t.y;
   }
-  *total = sum;
-  return before + incl - v;
+  return pre;
 }
 
-// All threads: the batch's cost, this CTA's range [cs, ce) of it, and the records that meet it,
-// without the first `skip`. CTA 0 also writes the plan for the joining kernel (skip 0).
+__device__ __forceinline__ int cost_of(const Args& a, int pages) {
+  return pages > 0 ? a.Hkv * (pages + a.overhead) : 0;
+}
+
+__device__ __forceinline__ Split make_split(const Args& a, int total) {
+  Split sp;
+  sp.total = total;
+  sp.ctas = min(static_cast<int>(gridDim.x), (total + a.min_cost - 1) / a.min_cost);
+  sp.quot = sp.ctas > 0 ? total / sp.ctas : 0;
+  sp.rem = total - sp.quot * sp.ctas;
+  return sp;
+}
+
+__device__ __forceinline__ void write_plan(const Args& a, const Rec& r, bool bad, int b) {
+  if (bad) set_err(a.err, LSA_DEVERR_BAD_SIZE);
+  Plan p;
+  p.base = r.base;
+  p.pages = r.pages;
+  p.n = r.n;
+  p.e1 = r.e1;
+  p.e2 = r.e2;
+  p.pad0 = p.pad1 = p.pad2 = 0;
+  a.plan[b] = p;
+}
+
+// All threads: the split of the batch's cost, this CTA's range of it, and the records that meet
+// the range, without the first `skip`. CTA 0 also writes the plan for the joining kernel. Ends
+// with a block-wide barrier. A dry run (B = 0) only brings the code into the instruction cache:
+// the plan is straight-line code that runs once, and fetching it costs more than running it.
 template <int HP>
-__device__ __noinline__ void plan_cta(const Args& a, int skip, Misc<HP>* m, int tid, int& cs, int& ce) {
-  constexpr unsigned long long RANK = 1ull << 32;     // high word: sequences with any cost
-  const bool one = a.B <= NTHREADS;                   // one sequence per thread: read it once
+__device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int skip, Misc<HP>* m, int tid) {
+  const int lane = tid & 31;
+  const int cta = blockIdx.x;
+  const bool write = cta == 0 && skip == 0 && !dry;
   Rec r;
   bool bad = false;
   r.pages = 0;
-  unsigned long long pre = 0, total = 0;
-  if (one) {
-    if (tid < a.B) r = read_seq(a, tid, bad);
-    pre = block_scan(r.pages > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.pages + a.overhead)) : 0ull, m, tid, &total);
-  } else {
-    unsigned long long mine = 0;
-    for (int b = tid; b < a.B; b += NTHREADS) {
-      const int pages = read_seq(a, b, bad).pages;
-      if (pages > 0) mine += static_cast<unsigned>(a.Hkv * (pages + a.overhead));
+  if (B <= 32) {
+    // a warp holds the batch, and its hits fit the records
+    if (tid < 32) {
+      if (lane < B) r = read_seq(a, lane, bad);
+      const int cost = cost_of(a, r.pages);
+      int incl = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const Split sp = make_split(a, __shfl_sync(0xffffffffu, incl, 31));
+      const int cs = cta < sp.ctas ? sp.start(cta) : 0, ce = cta < sp.ctas ? sp.start(cta + 1) : 0;
+      r.base = incl - cost;
+      const bool hit = cost > 0 && r.base < ce && incl > cs;
+      const unsigned mask = __ballot_sync(0xffffffffu, hit);
+      if (hit) m->rec[__popc(mask & ((1u << lane) - 1u))] = r;
+      if (lane == 0) {
+        m->nrec = __popc(mask);
+        m->more = 0;
+        m->cs = cs;
+        m->ce = ce;
+        if (write) *a.split = sp;
+      }
+      if (write && lane < B) write_plan(a, r, bad, lane);
     }
-    block_scan(mine, m, tid, &total);
+    __syncthreads();
+    return;
   }
-  Split sp;
-  sp.total = static_cast<int>(total & 0xffffffffu);
-  sp.ctas = min(static_cast<int>(gridDim.x), (sp.total + a.min_cost - 1) / a.min_cost);
-  sp.quot = sp.ctas > 0 ? sp.total / sp.ctas : 0;
-  sp.rem = sp.total - sp.quot * sp.ctas;
-  const int cta = blockIdx.x;
-  cs = ce = 0;
-  if (cta < sp.ctas) {
-    cs = sp.start(cta);
-    ce = sp.start(cta + 1);
+  const bool one = B <= NTHREADS;                     // one sequence per thread: read it once
+  int2 pre = make_int2(0, 0), tot;
+  if (one) {
+    if (tid < B) r = read_seq(a, tid, bad);
+    pre = block_scan(cost_of(a, r.pages), r.pages > 0, m, tid, tot);
+  } else {
+    int mine = 0;
+    for (int b = tid; b < B; b += NTHREADS) mine += cost_of(a, read_seq(a, b, bad).pages);
+    block_scan(mine, false, m, tid, tot);
   }
-  const bool write = cta == 0 && skip == 0;
-  if (write && tid == 0) *a.split = sp;
-  if (tid == 0) m->rank0 = m->rank1 = 0;              // (a CTA without any range)
-  unsigned long long base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += NTHREADS) {
+  const Split sp = make_split(a, tot.x);
+  const int cs = cta < sp.ctas ? sp.start(cta) : 0, ce = cta < sp.ctas ? sp.start(cta + 1) : 0;
+  if (tid == 0) {
+    m->rank0 = m->rank1 = 0;                          // (a CTA without any range)
+    m->cs = cs;
+    m->ce = ce;
+    if (write) *a.split = sp;
+  }
+  int2 base = make_int2(0, 0);
+  for (int b0 = 0; b0 < B; b0 += NTHREADS) {
     const int b = b0 + tid;
     if (!one) {
       r.pages = 0;
       bad = false;
-      if (b < a.B) r = read_seq(a, b, bad);
-      pre = block_scan(r.pages > 0 ? RANK + static_cast<unsigned>(a.Hkv * (r.pages + a.overhead)) : 0ull, m, tid, &total);
+      if (b < B) r = read_seq(a, b, bad);
+      pre = block_scan(cost_of(a, r.pages), r.pages > 0, m, tid, tot);
+      pre.x += base.x;
+      pre.y += base.y;
+      base.x += tot.x;
+      base.y += tot.y;
     }
-    pre += base;
-    base += total;
-    const int first = static_cast<int>(pre & 0xffffffffu), rank = static_cast<int>(pre >> 32);
-    const int behind = first + a.Hkv * (r.pages + a.overhead);
-    const bool live = b < a.B && r.pages > 0;
-    r.base = first;
-    if (write && b < a.B) {
-      if (bad) set_err(a.err, LSA_DEVERR_BAD_SIZE);
-      Plan p;
-      p.base = first;
-      p.pages = r.pages;
-      p.n = r.n;
-      p.e1 = r.e1;
-      p.e2 = r.e2;
-      p.pad0 = p.pad1 = p.pad2 = 0;
-      a.plan[b] = p;
-    }
-    const bool hit = live && first < ce && behind > cs;
+    const int behind = pre.x + cost_of(a, r.pages);
+    r.base = pre.x;
+    if (write && b < B) write_plan(a, r, bad, b);
+    const bool hit = b < B && r.pages > 0 && pre.x < ce && behind > cs;
     __syncthreads();
-    if (hit && first <= cs) m->rank0 = rank;          // the record that holds cs
-    if (hit && behind >= ce) m->rank1 = rank + 1;
+    if (hit && pre.x <= cs) m->rank0 = pre.y;         // the record that holds cs
+    if (hit && behind >= ce) m->rank1 = pre.y + 1;
     __syncthreads();
-    const int idx = rank - m->rank0 - skip;
+    const int idx = pre.y - m->rank0 - skip;
     if (hit && idx >= 0 && idx < MAXREC) m->rec[idx] = r;
   }
   __syncthreads();
@@ -514,23 +558,25 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     tmem_relinquish();
   }
   warm_up(a, tid);
-  tc_fence_before();
-  // Launched as a programmatic dependent: nothing a preceding kernel may write is read or
-  // written before this point.
-  grid_dependency_wait();
-  grid_dependents_launch();
-  int cs, ce;
-  plan_cta<HP>(a, 0, m, tid, cs, ce);      // ends with a block-wide barrier
-  tc_fence_after();
-  const uint32_t tmem = m->tmem_base;
-
   int ring_pos = 0;      // stages armed (producer) or consumed (MMA); softmax: stages before the segment
   int seg_count = 0;     // segments started by this role
   int gtile_s = 0;       // S tiles issued / read
   int gtile_o = 0;       // PV tiles issued / P tiles written
   int n_clean = 0;       // tiles with rows to clear so far (MMA)
-  for (int batch = 0;; ++batch) {
-    const int nrec = m->nrec;
+  tc_fence_before();
+  for (int batch = -1;; ++batch) {
+    const bool dry = batch < 0;
+    plan_cta<HP>(a, dry ? 0 : a.B, dry, batch * MAXREC, m, tid);
+    if (dry) {
+      // Launched as a programmatic dependent: nothing a preceding kernel may write is read or
+      // written before this point.
+      grid_dependency_wait();
+      grid_dependents_launch();
+      continue;
+    }
+    tc_fence_after();
+    const uint32_t tmem = m->tmem_base;
+    const int nrec = m->nrec, cs = m->cs, ce = m->ce;
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       const uint64_t evict_first = l2_policy_evict_first();
@@ -1003,7 +1049,6 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     tc_fence_after();
     if (!m->more || *abort) break;
     __syncthreads();
-    plan_cta<HP>(a, (batch + 1) * MAXREC, m, tid, cs, ce);
   }
   // ---------------------------------------------------------------- teardown
   if (*abort) {
@@ -1023,7 +1068,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, LY::TMEM_COLS);
+  if (warp == 1) tmem_dealloc(m->tmem_base, LY::TMEM_COLS);
 }
 
 // ------------------------------------------------------------------------ joining

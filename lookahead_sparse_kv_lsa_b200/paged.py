@@ -18,8 +18,11 @@ _DTYPES = {torch.bfloat16: _lib.DTYPE_BF16, torch.float16: _lib.DTYPE_F16}
 
 
 def _check(t, dtype, name: str, shape, device) -> Optional[int]:
-    """The tensor's address; ValueError unless it is a contiguous tensor of this type, shape
-    (None: any extent) and device."""
+    """The tensor's address; ValueError unless it is a contiguous tensor of this type, shape and
+    device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -28,11 +31,9 @@ def _check(t, dtype, name: str, shape, device) -> Optional[int]:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 class LsaPagedTables:
@@ -63,7 +64,7 @@ class LsaPagedTables:
             _check(score, torch.float32, "score", (B, E), dev),
             _check(n_entries, i32, "n_entries", (B,), dev),
             _check(tail_len, i32, "tail_len", (B,), dev),
-            _check(free_list, i32, "free_list", (B, None), dev),
+            _check(free_list, i32, "free_list", (B, self.free_stride), dev),
             _check(free_cnt, i32, "free_cnt", (B,), dev))
 
     @classmethod
@@ -127,27 +128,27 @@ class LsaPagedCache:
         s.ws, s.ws_bytes = self.ws.data_ptr(), size
         self.state = s
         self._ref = C.byref(s)
+        self._calls = {f: getattr(self._lib, f)
+                       for f in ("lsa_paged_attn", "lsa_paged_append", "lsa_paged_evict")}
+        self._q_shape = torch.Size((B, int(H), d))
 
     def _call(self, name: str, stream, *args) -> None:
         """One library call on `stream` (default: the current stream of the cache's device),
         with that device current."""
-        f = getattr(self._lib, name)
-        if torch.cuda.current_device() == self.device.index:
-            st = f(self._ref, *args, self._stream(stream))
-        else:
-            with torch.cuda.device(self.device):
-                st = f(self._ref, *args, self._stream(stream))
-        if st:
-            _lib.check(name, st)
-
-    def _stream(self, stream) -> int:
+        f, index = self._calls[name], self.device.index
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        if isinstance(stream, torch.cuda.Stream):
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        elif isinstance(stream, torch.cuda.Stream):
             if stream.device != self.device:
                 raise ValueError("the stream is on %s, the cache on %s" % (stream.device, self.device))
-            return stream.cuda_stream
-        return int(stream)
+            stream = stream.cuda_stream
+        if torch._C._cuda_getDevice() == index:
+            st = f(self._ref, *args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = f(self._ref, *args, stream)
+        if st:
+            _lib.check(name, st)
 
     def _dst(self, dst: Optional[LsaPagedTables]):
         if dst is None:
@@ -160,9 +161,8 @@ class LsaPagedCache:
     def attend(self, q, out, stream=None) -> None:
         """One new token of every sequence over the cache (lsa_paged_attn). q, out: [B][H][d];
         adds the pages' weights to the tables' scores."""
-        shape = (self.B, self.H, self.d)
-        self._call("lsa_paged_attn", stream, _check(q, self.dtype, "q", shape, self.device),
-                   _check(out, self.dtype, "out", shape, self.device))
+        self._call("lsa_paged_attn", stream, _check(q, self.dtype, "q", self._q_shape, self.device),
+                   _check(out, self.dtype, "out", self._q_shape, self.device))
 
     def append(self, k, v, tok_off=None, dst: Optional[LsaPagedTables] = None, stream=None) -> None:
         """New tokens behind every sequence's last (lsa_paged_append). k, v: [tokens][Hkv][d];
