@@ -80,9 +80,14 @@ struct Split {
   }
 };
 
-// What the joining kernel needs of a sequence (workspace, written by CTA 0).
+// What the joining kernel needs: of a sequence (written by CTA 0), and of a pair, its first
+// part's slot and the number of parts (written by the CTA of its first segment, or, where
+// nothing is seen, by CTA 0).
 struct Plan {
-  int base, pages, n, e1, e2, pad0, pad1, pad2;
+  int pages, n, e1, e2;
+};
+struct Pair {
+  int slot, parts;
 };
 
 struct Args {
@@ -96,13 +101,14 @@ struct Args {
   float* score;
   uint16_t* out;
   int32_t* err;
-  Split* split;      // workspace
-  Plan* plan;        // [B]
-  float2* part_ml;   // [slot][G] running max (log2 units) and sum
-  float* part_o;     // [slot][G][d]
+  Plan* plan;        // workspace: [B]
+  Pair* pair;        // [B][Hkv]
+  float2* part_ml;   // [G][slots] running max (log2 units) and sum
+  float* part_o;     // [slot][d/128][G][128]
   float2* half_w;    // [B][bt_stride][2][H] half pages' sums and the max they refer to
   long long n_pages;
   int B, H, Hkv, G, d, bt_stride, window, f16;
+  int slots;         // of the workspace's parts
   int min_cost;      // least cost worth a CTA
   int overhead;      // cost of a segment besides its pages
   float scale, cap, decay;
@@ -201,6 +207,7 @@ struct Seg {
 // same. A key head's range starts with its overhead, then come its pages.
 struct SegWalk {
   int kvh, end, at;       // next key head, heads, cost position of its first page
+  int seg_at;             // cost position of the first page of the last segment's pair
   int cs, ce, step;
   __device__ __forceinline__ void start(const Rec& r, int cs_, int ce_, const Args& a) {
     cs = cs_;
@@ -215,6 +222,7 @@ struct SegWalk {
       s.kvh = kvh++;
       s.u0 = max(0, cs - at);
       s.u1 = min(r.pages, ce - at);
+      seg_at = at;
       at += step;
       if (s.u1 > s.u0) return true;
     }
@@ -249,6 +257,7 @@ struct Misc {
   int abort;
   int nrec, more, rank0, rank1;
   int cs, ce;                      // the CTA's cost range
+  Split split;
   int2 wsum[NTHREADS / 32];
   Rec rec[MAXREC];
   int y[YRING];
@@ -305,13 +314,16 @@ __device__ __forceinline__ Split make_split(const Args& a, int total) {
 __device__ __forceinline__ void write_plan(const Args& a, const Rec& r, bool bad, int b) {
   if (bad) set_err(a.err, LSA_DEVERR_BAD_SIZE);
   Plan p;
-  p.base = r.base;
   p.pages = r.pages;
   p.n = r.n;
   p.e1 = r.e1;
   p.e2 = r.e2;
-  p.pad0 = p.pad1 = p.pad2 = 0;
   a.plan[b] = p;
+  if (r.pages == 0) {
+    Pair none;
+    none.slot = none.parts = 0;
+    for (int g = 0; g < a.Hkv; ++g) a.pair[static_cast<long long>(b) * a.Hkv + g] = none;
+  }
 }
 
 // All threads: the split of the batch's cost, this CTA's range of it, and the records that meet
@@ -348,7 +360,7 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
         m->more = 0;
         m->cs = cs;
         m->ce = ce;
-        if (write) *a.split = sp;
+        m->split = sp;
       }
       if (write && lane < B) write_plan(a, r, bad, lane);
     }
@@ -371,7 +383,7 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
     m->rank0 = m->rank1 = 0;                          // (a CTA without any range)
     m->cs = cs;
     m->ce = ce;
-    if (write) *a.split = sp;
+    m->split = sp;
   }
   int2 base = make_int2(0, 0);
   for (int b0 = 0; b0 < B; b0 += NTHREADS) {
@@ -999,28 +1011,58 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           // workspace: the pages' weights are normalised by them.
           const bool whole = sg.u0 == 0 && sg.u1 == r.pages;
           const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(r.b) * a.Hkv + sg.kvh;
+          if (t128 == 127 && sg.u0 == 0) {
+            Pair pr;
+            pr.slot = static_cast<int>(slot);
+            pr.parts = whole ? 1 : m->split.holder(walk.seg_at + r.pages - 1) - static_cast<int>(blockIdx.x) + 1;
+            a.pair[static_cast<long long>(r.b) * a.Hkv + sg.kvh] = pr;
+          }
           if (t128 < G) {
             const float sum = m->red[0][t128] + m->red[1][t128] + m->red[2][t128] + m->red[3][t128];
-            a.part_ml[slot * G + t128] = make_float2(m->m_raw[t128], sum);
+            a.part_ml[static_cast<long long>(t128) * a.slots + slot] = make_float2(m->m_raw[t128], sum);
             m->alpha[t128] = sum == 0.f ? 0.f : 1.f / sum;
           }
           named_bar_sync(1, 128);
-          // Lanes hold one dim of every head. Quads exchange 4 x 4 so that a lane holds 4 dims of
-          // one head: a store of a warp then covers 32 dims of 4 heads, whole 128-byte lines.
-          const int quad = lane >> 2, i4 = lane & 3;
-          uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0 + i4) * a.d + sw * 32 + quad * 4;
-          float* po = a.part_o + (slot * G + i4) * a.d + sw * 32 + quad * 4;
+          float* part = a.part_o + slot * G * a.d;
+          SegWalk ahead = walk;
+          Seg none;
+          if (!whole && ri == nrec - 1 && !m->more && !ahead.next(r, none)) {
+            // The CTA's last segment: the ring is idle, so each 128-dim block is laid out there
+            // as it goes to memory, [head][128], and stored by one bulk copy.
+            const uint32_t base = smem_u32(sRing) + row * 4;
 #pragma unroll 1
-          for (int db = 0; db < NDB; ++db, fo += 128, po += 128) {
-            float o[HP];
-            tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
-            tmem_wait_ld();
-            // no branch inside the common loop, so that its shuffles overlap
-            if (G == HP && !whole) {
+            for (int db = 0; db < NDB; ++db) {
+              float o[HP];
+              tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
+              tmem_wait_ld();
+              const uint32_t to = base + db * G * 512;
+              if (G == HP) {              // no branch between the common case's stores
 #pragma unroll
-              for (int h = 0; h < HP; h += 4)
-                *reinterpret_cast<float4*>(po + h * a.d) = quad_transpose(o[h], o[h + 1], o[h + 2], o[h + 3], i4);
-            } else {
+                for (int h = 0; h < HP; ++h) st_shared_f32(to + h * 512, o[h]);
+              } else {
+#pragma unroll
+                for (int h = 0; h < HP; ++h)
+                  if (h < G) st_shared_f32(to + h * 512, o[h]);
+              }
+              fence_proxy_async_smem();
+              named_bar_sync(1, 128);
+              if (t128 == 0) bulk_store(part + db * G * 128, sRing + db * G * 512, G * 512);
+            }
+            if (t128 == 0) {
+              bulk_commit_and_wait();
+              fence_proxy_async_global();
+            }
+          } else {
+            // Lanes hold one dim of every head. Quads exchange 4 x 4 so that a lane holds 4 dims
+            // of one head: a store of a warp then covers 32 dims of 4 heads, whole 128-byte lines.
+            const int quad = lane >> 2, i4 = lane & 3;
+            uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0 + i4) * a.d + sw * 32 + quad * 4;
+            float* po = part + i4 * 128 + sw * 32 + quad * 4;
+#pragma unroll 1
+            for (int db = 0; db < NDB; ++db, fo += 128, po += G * 128) {
+              float o[HP];
+              tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
+              tmem_wait_ld();
 #pragma unroll
               for (int h = 0; h < HP; h += 4) {
                 if (h < G) {
@@ -1031,7 +1073,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                       *reinterpret_cast<uint2*>(fo + h * a.d) =
                           make_uint2(pack16(v.x * inv, v.y * inv, f16), pack16(v.z * inv, v.w * inv, f16));
                     } else {
-                      *reinterpret_cast<float4*>(po + h * a.d) = v;
+                      *reinterpret_cast<float4*>(po + h * 128) = v;
                     }
                   }
                 }
@@ -1080,17 +1122,6 @@ struct JoinArgs {
 };
 
 constexpr int JOIN_WARPS = JOIN_THREADS / 32;
-constexpr int WARP_PARTS = 32;   // weights a warp keeps in its lanes at a time
-
-// Parts of head h of sequence b: their number (0: nothing seen) and the first one's slot.
-__device__ __forceinline__ int parts_of(const Args& a, const Split& sp, const Plan& p, int b, int kvh, long long& slot) {
-  if (p.pages <= 0) return 0;
-  const int at = p.base + kvh * (p.pages + a.overhead) + a.overhead;
-  const int c0 = sp.holder(at), c1 = sp.holder(at + p.pages - 1);
-  slot = c0 + static_cast<long long>(b) * a.Hkv + kvh;
-  return c1 - c0 + 1;
-}
-
 // A part that saw nothing has weight 0 (its max is -inf), and its values are dropped whatever
 // they are.
 __device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
@@ -1112,47 +1143,49 @@ __device__ __forceinline__ void store_out(uint16_t* p, float4 v, float inv, bool
 }
 
 // out[b][h] = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the parts of a head. A warp or a
-// block takes 128 dims of one head, 4 per lane, so a part is one 512-byte read of a warp.
+// block takes 128 dims of one head, 4 per lane, so a part is one 512-byte read of a warp. Every
+// warp forms all the weights itself, while its first parts are on their way. Two blocks per SM
+// and more fit beside each other, so that no block waits for another to end.
 //
 // The pages' weights are sums over half pages relative to the max at the time: score = decay *
 // score + sum over heads of (sum) 2^(m - M_h) / L_h.
-__global__ void __launch_bounds__(JOIN_THREADS)
+__global__ void __launch_bounds__(JOIN_THREADS, 4)
     paged_join_kernel(const __grid_constant__ Args a, const __grid_constant__ JoinArgs ja) {
   extern __shared__ float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.G;
   const bool f16 = a.f16 != 0;
-  if (tid == 0) prefetch_l2(a.split);
+  if (tid == 0) prefetch_l2(a.plan);
   if (tid == 1) prefetch_l2(a.part_o);
   if (tid == 2) prefetch_l2(a.out);
   if (tid == 3 && a.score) prefetch_l2(a.score);
+  const bool outs = static_cast<int>(blockIdx.x) < ja.out_blocks;
+  const int chunks = a.d / 128;
+  const int job = ja.wide ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
+  const int item = job / chunks, chunk = job - item * chunks;
+  const int ob = item / a.H, oh = item - ob * a.H, okv = oh / G;
   grid_dependency_wait();
   grid_dependents_launch();
-  const Split sp = *a.split;
-  if (static_cast<int>(blockIdx.x) < ja.out_blocks) {
-    const int chunks = a.d / 128;
-    const int job = ja.wide ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
-    const int item = job / chunks, chunk = job - item * chunks;
-    const int b = item / a.H, h = item - b * a.H, kvh = h / G;
-    if (b >= a.B) return;
-    long long slot = 0;
-    const int n = parts_of(a, sp, a.plan[b], b, kvh, slot);
+  if (outs) {
+    if (ob >= a.B) return;
+    const Pair pr = a.pair[static_cast<long long>(ob) * a.Hkv + okv];
+    const int n = pr.parts;
     if (n == 1) return;                         // written by the CTA that held the pair whole
     uint16_t* out = a.out + static_cast<long long>(item) * a.d + chunk * 128 + lane * 4;
     const long long stride = static_cast<long long>(G) * a.d;
-    const float2* ml = a.part_ml + slot * G + (h - kvh * G);
-    const float* part = a.part_o + slot * stride + (h - kvh * G) * a.d + chunk * 128 + lane * 4;
+    const float2* ml = a.part_ml + static_cast<long long>(oh - okv * G) * a.slots + pr.slot;
+    const float* part = a.part_o + pr.slot * stride + (chunk * G + oh - okv * G) * 128 + lane * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v[8];
     if (!ja.wide) {
       // -------- a warp: the running max over rounds of 32 parts, lane k holding part k's weight
       float top = -INFINITY, sum = 0.f;
-      for (int k0 = 0; k0 < n; k0 += WARP_PARTS) {
-        const int left = min(WARP_PARTS, n - k0);
-        float4 v[8];
+      for (int k0 = 0; k0 < n; k0 += 32) {
+        const int left = min(32, n - k0);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (e < left) v[e] = *reinterpret_cast<const float4*>(part + (k0 + e) * stride);
-        const float2 mine = lane < left ? ml[static_cast<long long>(k0 + lane) * G] : make_float2(-INFINITY, 0.f);
+        const float2 mine = lane < left ? ml[k0 + lane] : make_float2(-INFINITY, 0.f);
         float t = mine.x;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
@@ -1185,59 +1218,41 @@ __global__ void __launch_bounds__(JOIN_THREADS)
       return;
     }
     // -------- a block: every warp takes every 8th part
-    if (n == 0) {
-      if (warp == 0) store_out(out, acc, 0.f, f16);
-      return;
-    }
-    float* w = sm;                              // [n]
-    float4* acc_s = reinterpret_cast<float4*>(sm + MAX_CTAS);
-    float* red = sm + MAX_CTAS + 4 * JOIN_THREADS;
-    float4 v[10];                               // this warp's first parts, before the weights
 #pragma unroll
-    for (int e = 0; e < 10; ++e)
+    for (int e = 0; e < 8; ++e)
       if (warp + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (warp + e * JOIN_WARPS) * stride);
     float top = -INFINITY;
-    float2 mine[MAX_CTAS / JOIN_THREADS];
-#pragma unroll
-    for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
-      const int k = tid + i * JOIN_THREADS;
-      mine[i] = k < n ? ml[static_cast<long long>(k) * G] : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, mine[i].x);
-    }
+#pragma unroll 5
+    for (int k = lane; k < n; k += 32) top = fmaxf(top, ml[k].x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < JOIN_WARPS; ++i) top = fmaxf(top, red[i]);
+    // all warps write the same weights to the same words, and each reads its own writes
+    float* w = sm;
     float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < MAX_CTAS / JOIN_THREADS; ++i) {
-      const int k = tid + i * JOIN_THREADS;
-      const float wk = part_weight(mine[i].x, top);
-      if (k < n) w[k] = wk;
-      sum += wk == 0.f ? 0.f : wk * mine[i].y;
+#pragma unroll 5
+    for (int k = lane; k < n; k += 32) {
+      const float2 x = ml[k];
+      const float wk = part_weight(x.x, top);
+      w[k] = wk;
+      sum += wk == 0.f ? 0.f : wk * x.y;
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red[JOIN_WARPS + warp] = sum;
-    __syncthreads();
-    for (int k = warp; k < n; k += 10 * JOIN_WARPS) {
+    __syncwarp();
+    for (int k = warp; k < n; k += 8 * JOIN_WARPS) {
       if (k > warp) {
 #pragma unroll
-        for (int e = 0; e < 10; ++e)
+        for (int e = 0; e < 8; ++e)
           if (k + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (k + e * JOIN_WARPS) * stride);
       }
 #pragma unroll
-      for (int e = 0; e < 10; ++e)
+      for (int e = 0; e < 8; ++e)
         if (k + e * JOIN_WARPS < n) add_part(acc, w[k + e * JOIN_WARPS], v[e]);
     }
+    float4* acc_s = reinterpret_cast<float4*>(sm + MAX_CTAS);
     acc_s[tid] = acc;
     __syncthreads();
     if (warp == 0) {
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < JOIN_WARPS; ++i) sum += red[JOIN_WARPS + i];
 #pragma unroll
       for (int i = 1; i < JOIN_WARPS; ++i) add_part(acc, 1.f, acc_s[i * 32 + lane]);
       store_out(out, acc, sum == 0.f ? 0.f : 1.f / sum, f16);
@@ -1250,52 +1265,55 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   const Plan p = a.plan[b];
   if (j0 >= p.n) return;
   float2* fin = reinterpret_cast<float2*>(sm);                 // [H]: (M, 1 / L)
-  float2* tmp = fin + a.H;                                     // [JOIN_THREADS]
   if (p.pages > 0) {
-    // threads over (part, head), heads fastest: consecutive threads read consecutive words
-    const int per = a.H < JOIN_THREADS ? JOIN_THREADS / a.H : 1;   // parts read side by side
-    for (int h0 = 0; h0 < a.H; h0 += JOIN_THREADS) {
-      const int s = a.H < JOIN_THREADS ? tid / a.H : 0;
-      const int h = a.H < JOIN_THREADS ? tid - s * a.H : h0 + tid;
-      float M = -INFINITY, L = 0.f;
-      if (h < a.H && s < per) {
-        const int kvh = h / G;
-        long long slot = 0;
-        const int n = parts_of(a, sp, p, b, kvh, slot);
-        const float2* ml = a.part_ml + slot * G + (h - kvh * G);
-        for (int k = s; k < n; k += 16 * per) {
-          float2 v[16];
-          float t = M;
+    // a warp takes four heads at a time, a lane every 32nd part
+    for (int h0 = 4 * warp; h0 < a.H; h0 += 4 * JOIN_WARPS) {
+      float M[4], L[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[e] = k + e * per < n ? ml[static_cast<long long>(k + e * per) * G] : make_float2(-INFINITY, 0.f);
-            t = fmaxf(t, v[e].x);
-          }
-          L *= part_weight(M, t);
-          M = t;
+      for (int e = 0; e < 4; ++e) {
+        M[e] = -INFINITY;
+        L[e] = 0.f;
+      }
+      const float2* ml[4];
+      int n[4], most = 0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float w = part_weight(v[e].x, M);
-            if (w != 0.f) L = fmaf(w, v[e].y, L);
-          }
+      for (int e = 0; e < 4; ++e) {
+        const int h = min(h0 + e, a.H - 1), kvh = h / G;
+        const Pair pr = a.pair[static_cast<long long>(b) * a.Hkv + kvh];
+        ml[e] = a.part_ml + static_cast<long long>(h - kvh * G) * a.slots + pr.slot;
+        n[e] = pr.parts;
+        most = max(most, n[e]);
+      }
+      for (int k = lane; k < most; k += 64) {
+        float2 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = k + 32 * (e & 1);
+          v[e] = i < n[e / 2] ? ml[e / 2][i] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float t = fmaxf(M[e], fmaxf(v[2 * e].x, v[2 * e + 1].x));
+          L[e] *= part_weight(M[e], t);
+          M[e] = t;
+          const float w0 = part_weight(v[2 * e].x, t), w1 = part_weight(v[2 * e + 1].x, t);
+          if (w0 != 0.f) L[e] = fmaf(w0, v[2 * e].y, L[e]);
+          if (w1 != 0.f) L[e] = fmaf(w1, v[2 * e + 1].y, L[e]);
         }
       }
-      tmp[tid] = make_float2(M, L);
-      __syncthreads();
-      if (s == 0 && h < a.H) {
-        if (per > 1) {                       // (a.H < JOIN_THREADS)
-          for (int i = 1; i < per; ++i) M = fmaxf(M, tmp[i * a.H + h].x);
-          L = 0.f;
-          for (int i = 0; i < per; ++i) {
-            const float2 v = tmp[i * a.H + h];
-            const float w = part_weight(v.x, M);
-            if (w != 0.f) L = fmaf(w, v.y, L);
-          }
-        }
-        fin[h] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float t = M[e];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        const float w = part_weight(M[e], t);
+        float l = w == 0.f ? 0.f : L[e] * w;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0 && h0 + e < a.H) fin[h0 + e] = make_float2(t, l == 0.f ? 0.f : 1.f / l);
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
   // a warp takes four entries at a time, so that their loads overlap
   const int j1 = min(p.n, j0 + ja.entries);
@@ -1340,7 +1358,7 @@ using lsa::paged::JoinArgs;
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct WsLayout {
-  size_t split, plan, ml, o, half, bytes;
+  size_t slots, plan, pair, ml, o, half, bytes;
 };
 
 // Slots: one per CTA and one per (sequence, key head) pair.
@@ -1348,9 +1366,10 @@ WsLayout ws_layout(int B, int H, int Hkv, int d, int bt_stride, bool with_score,
   const size_t G = static_cast<size_t>(H) / Hkv;
   const size_t slots = 2 * static_cast<size_t>(n_sm) + static_cast<size_t>(B) * Hkv;
   WsLayout w;
-  w.split = 0;
-  w.plan = 256;
-  w.ml = w.plan + up256(static_cast<size_t>(B) * sizeof(lsa::paged::Plan));
+  w.slots = slots;
+  w.plan = 0;
+  w.pair = up256(static_cast<size_t>(B) * sizeof(lsa::paged::Plan));
+  w.ml = w.pair + up256(static_cast<size_t>(B) * Hkv * sizeof(lsa::paged::Pair));
   w.o = w.ml + up256(slots * G * sizeof(float2));
   w.half = w.o + up256(slots * G * d * sizeof(float));
   w.bytes = w.half + (with_score ? up256(static_cast<size_t>(B) * bt_stride * 2 * H * sizeof(float2)) : 0);
@@ -1405,8 +1424,8 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
     ja.chunks = static_cast<int>((a.bt_stride + per - 1) / per);
     blocks += static_cast<long long>(a.B) * ja.chunks;
   }
-  const size_t sm_wide = (lsa::paged::MAX_CTAS + 4 * lsa::paged::JOIN_THREADS + 16) * sizeof(float);
-  const size_t sm_score = a.score ? (static_cast<size_t>(a.H) + lsa::paged::JOIN_THREADS) * sizeof(float2) : 0;
+  const size_t sm_wide = lsa::paged::MAX_CTAS * sizeof(float) + lsa::paged::JOIN_THREADS * sizeof(float4);
+  const size_t sm_score = a.score ? static_cast<size_t>(a.H) * sizeof(float2) : 0;
   size_t smem = ja.wide ? sm_wide : 0;
   if (sm_score > smem) smem = sm_score;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -1494,8 +1513,8 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   a.out = out;
   a.err = c->err;
   uint8_t* ws = static_cast<uint8_t*>(c->ws);
-  a.split = reinterpret_cast<lsa::paged::Split*>(ws + w.split);
   a.plan = reinterpret_cast<lsa::paged::Plan*>(ws + w.plan);
+  a.pair = reinterpret_cast<lsa::paged::Pair*>(ws + w.pair);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
   a.half_w = reinterpret_cast<float2*>(ws + w.half);
@@ -1508,6 +1527,7 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   a.bt_stride = c->bt_stride;
   a.window = c->window;
   a.f16 = c->dtype == LSA_DTYPE_F16;
+  a.slots = static_cast<int>(w.slots);
   a.scale = c->scale;
   a.cap = c->cap;
   a.decay = c->decay;

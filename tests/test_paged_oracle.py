@@ -159,7 +159,7 @@ def test_workspace_size(lib):
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
     for B, H, Hkv, d, E in ((1, 64, 1, 512, 16385), (64, 64, 8, 128, 64), (3, 21, 7, 256, 1)):
         slots, G = 2 * 148 + B * Hkv, H // Hkv
-        base = 256 + up(B * 32) + up(slots * G * 8) + up(slots * G * d * 4)
+        base = up(B * 16) + up(B * Hkv * 8) + up(slots * G * 8) + up(slots * G * d * 4)
         assert f(B, H, Hkv, d, E, 0, 148) == base
         assert f(B, H, Hkv, d, E, 1, 148) == base + up(B * E * 2 * H * 8)
     for bad in ((0, 8, 1, 128, 4), (1, 9, 2, 128, 4), (1, 65, 1, 128, 4), (1, 8, 1, 100, 4), (1, 8, 1, 128, 0)):
