@@ -69,12 +69,14 @@ struct Rec {
   int masked;        // whether low / pre exclude any position of a seen entry
 };
 
-// The split: `total` cost units over `ctas` CTAs, the first `rem` of them with quot + 1.
+// The split: the cost positions from `off` on over `ctas` CTAs, the first `rem` of them with
+// quot + 1.
 struct Split {
-  int total, ctas, quot, rem;
-  __device__ __forceinline__ int start(int cta) const { return cta * quot + min(cta, rem); }
+  int off, ctas, quot, rem;
+  __device__ __forceinline__ int start(int cta) const { return off + cta * quot + min(cta, rem); }
   // CTA that holds cost position x
   __device__ __forceinline__ int holder(int x) const {
+    x -= off;
     const int big = rem * (quot + 1);
     return x < big ? x / (quot + 1) : rem + (x - big) / quot;
   }
@@ -109,7 +111,7 @@ struct Args {
   long long n_pages;
   int B, H, Hkv, G, d, bt_stride, window, f16;
   int slots;         // of the workspace's parts
-  int min_cost;      // least cost worth a CTA
+  int min_pages;     // least share of pages worth a CTA
   int overhead;      // cost of a segment besides its pages
   float scale, cap, decay;
 };
@@ -302,12 +304,16 @@ __device__ __forceinline__ int cost_of(const Args& a, int pages) {
   return pages > 0 ? a.Hkv * (pages + a.overhead) : 0;
 }
 
-__device__ __forceinline__ Split make_split(const Args& a, int total) {
+// A CTA that goes on with a pair pays for one segment, and one that also starts the next pair
+// for one more: only the starts differ between CTAs, so only they are charged, and not the
+// batch's first.
+__device__ __forceinline__ Split make_split(const Args& a, int total, int seqs) {
   Split sp;
-  sp.total = total;
-  sp.ctas = min(static_cast<int>(gridDim.x), (total + a.min_cost - 1) / a.min_cost);
-  sp.quot = sp.ctas > 0 ? total / sp.ctas : 0;
-  sp.rem = total - sp.quot * sp.ctas;
+  sp.off = a.overhead;
+  sp.ctas = min(static_cast<int>(gridDim.x),
+                (total - seqs * a.Hkv * a.overhead + a.min_pages - 1) / a.min_pages);
+  sp.quot = sp.ctas > 0 ? (total - sp.off) / sp.ctas : 0;
+  sp.rem = total - sp.off - sp.quot * sp.ctas;
   return sp;
 }
 
@@ -349,7 +355,8 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
         const int t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
       }
-      const Split sp = make_split(a, __shfl_sync(0xffffffffu, incl, 31));
+      const Split sp = make_split(a, __shfl_sync(0xffffffffu, incl, 31),
+                                  __popc(__ballot_sync(0xffffffffu, cost > 0)));
       const int cs = cta < sp.ctas ? sp.start(cta) : 0, ce = cta < sp.ctas ? sp.start(cta + 1) : 0;
       r.base = incl - cost;
       const bool hit = cost > 0 && r.base < ce && incl > cs;
@@ -373,11 +380,19 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
     if (tid < B) r = read_seq(a, tid, bad);
     pre = block_scan(cost_of(a, r.pages), r.pages > 0, m, tid, tot);
   } else {
-    int mine = 0;
-    for (int b = tid; b < B; b += NTHREADS) mine += cost_of(a, read_seq(a, b, bad).pages);
+    int mine = 0, seqs = 0;
+    for (int b = tid; b < B; b += NTHREADS) {
+      const int pages = read_seq(a, b, bad).pages;
+      mine += cost_of(a, pages);
+      seqs += pages > 0;
+    }
     block_scan(mine, false, m, tid, tot);
+    const int cost = tot.x;
+    block_scan(seqs, false, m, tid, tot);
+    tot.y = tot.x;
+    tot.x = cost;
   }
-  const Split sp = make_split(a, tot.x);
+  const Split sp = make_split(a, tot.x, tot.y);
   const int cs = cta < sp.ctas ? sp.start(cta) : 0, ce = cta < sp.ctas ? sp.start(cta + 1) : 0;
   if (tid == 0) {
     m->rank0 = m->rank1 = 0;                          // (a CTA without any range)
@@ -418,9 +433,9 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
   __syncthreads();
 }
 
-// Fixed cost of a segment in pages: 3 to 4 us of pipeline fill and drain, at the 1.5 us
-// (d = 128, two CTAs per SM) to 3 us (d = 512) that a page takes to load.
-__host__ __device__ constexpr int overhead_pages(int d) { return d >= 384 ? 1 : 2; }
+// Fixed cost of a segment in pages, and the least share of pages that a CTA is started for.
+__host__ __device__ constexpr int overhead_pages(int d) { return d >= 256 ? 6 : 8; }
+__host__ __device__ constexpr int least_pages(int d) { return d >= 256 ? 1 : 2; }
 
 // Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
 // stage count is even. Up to 32 heads two CTAs share an SM (at most 113 KB each), so that one
@@ -1226,14 +1241,14 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
     for (int k = lane; k < n; k += 32) top = fmaxf(top, ml[k].x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // all warps write the same weights to the same words, and each reads its own writes
+    // each warp keeps the weights of its own parts, k = warp mod 8
     float* w = sm;
     float sum = 0.f;
 #pragma unroll 5
     for (int k = lane; k < n; k += 32) {
       const float2 x = ml[k];
       const float wk = part_weight(x.x, top);
-      w[k] = wk;
+      if ((lane & (JOIN_WARPS - 1)) == warp) w[k] = wk;
       sum += wk == 0.f ? 0.f : wk * x.y;
     }
 #pragma unroll
@@ -1387,10 +1402,8 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   auto kern = lsa::paged::paged_attn_kernel<HP, NDC>;
   const lsa_status st = lsa_host::ensure_smem_limit(reinterpret_cast<const void*>(kern), LY::SMEM);
   if (st != LSA_OK) return st;
-  // A segment's fixed cost in pages, and the least a CTA is started for, in pages besides it.
   a.overhead = lsa::paged::overhead_pages(NDC * 64);
-  const int min_pages = NDC >= 4 ? 1 : 2;
-  a.min_cost = min_pages + a.overhead;
+  a.min_pages = lsa::paged::least_pages(NDC * 64);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1401,7 +1414,7 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // no more CTAs than the largest tables could fill
-  const long long most = static_cast<long long>(a.B) * a.Hkv * ((static_cast<long long>(a.bt_stride) + min_pages - 1) / min_pages);
+  const long long most = static_cast<long long>(a.B) * a.Hkv * ((static_cast<long long>(a.bt_stride) + a.min_pages - 1) / a.min_pages);
   const long long ctas = static_cast<long long>(n_sm) * LY::CTAS_PER_SM;
   cfg.gridDim = dim3(static_cast<unsigned>(most < ctas ? most : ctas));
   if (cudaLaunchKernelEx(&cfg, kern, mkv, mq, a) != cudaSuccess) {
@@ -1472,7 +1485,7 @@ extern "C" lsa_status lsa_paged_check(const lsa_paged_cache* c) {
   if (!c->t.block_table || !c->t.n_entries || !c->t.tail_len || !c->err) return LSA_ERR_INVALID_ARG;
   if (c->free_stride > 0 && (!c->t.free_list || !c->t.free_cnt)) return LSA_ERR_INVALID_ARG;
   // the attention's cost positions are int32
-  if (static_cast<int64_t>(c->B) * c->Hkv * (static_cast<int64_t>(c->bt_stride) + 2) > (int64_t(1) << 30))
+  if (static_cast<int64_t>(c->B) * c->Hkv * (static_cast<int64_t>(c->bt_stride) + 16) > (int64_t(1) << 30))
     return LSA_ERR_INVALID_ARG;
   return LSA_OK;
 }
