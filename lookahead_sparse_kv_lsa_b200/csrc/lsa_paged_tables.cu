@@ -178,106 +178,287 @@ __device__ __forceinline__ uint32_t score_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_score(uint32_t k) {
+  // keys between 0 and that of -inf belong to no score: every score with a key is above them
+  if (k < 0x007fffffu) return -INFINITY;
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 struct EvictShared {
   int cnt[2][32];
   int cnt2[32];
 };
 
 // Sum of v over the block; one barrier, alternating buffers.
-__device__ __forceinline__ int block_sum(int v, EvictShared* s, int which, int warp, int lane, int nwarps) {
+__device__ __forceinline__ int block_sum(int v, EvictShared* s, int& which, int warp, int lane, int nwarps) {
   v = __reduce_add_sync(0xffffffffu, v);
+  if (nwarps == 1) return v;
   if (lane == 0) s->cnt[which][warp] = v;
   __syncthreads();
-  return __reduce_add_sync(0xffffffffu, lane < nwarps ? s->cnt[which][lane] : 0);
+  v = __reduce_add_sync(0xffffffffu, lane < nwarps ? s->cnt[which][lane] : 0);
+  which ^= 1;
+  return v;
 }
 
-// A CTA per sequence. The threshold, the (budget - sink - recent)-th largest key of the middle
-// entries, is found bit by bit from the top: the largest T such that at least that many keys
-// are >= T, one count of the block per bit. Keys stay in registers up to PER per thread;
-// longer rows read them again. Then chunks of blockDim entries are placed in order: kept
-// entries to the front, freed pages onto the stack. A chunk is read whole before any of it
-// is written, and entries only move towards the front, so dst may be src.
-constexpr int PER = 16;
+// The counts of sequence b, checked, and written to dst. Returns false where nothing is to be
+// trimmed (the row has then been copied).
+struct EvictRow {
+  int n, have, gone;
+};
+__device__ __forceinline__ bool evict_begin(const EvictArgs& a, int b, int tid, int nt, EvictRow& r) {
+  r.n = a.src.n_entries[b];
+  r.have = a.src.free_cnt[b];
+  const int tail = a.src.tail_len[b];
+  __syncthreads();                          // the counts are read before any thread writes them
+  int bits = 0;
+  if (r.n < 0 || r.n > a.bt_stride || r.have < 0 || r.have > a.free_stride) bits = LSA_DEVERR_BAD_SIZE;
+  r.gone = bits == 0 && r.n > a.budget ? r.n - a.budget : 0;
+  if (r.gone > a.free_stride - r.have && bits == 0) {
+    bits = LSA_DEVERR_POOL_CAPACITY;
+    r.gone = 0;
+  }
+  if (tid == 0) {
+    a.dst.n_entries[b] = r.n - r.gone;
+    a.dst.free_cnt[b] = r.have + r.gone;
+    a.dst.tail_len[b] = tail;
+    if (bits) set_err(a.err, bits);
+  }
+  if (bits == LSA_DEVERR_BAD_SIZE) return false;
+  if (r.gone > 0) return true;
+  const long long row = static_cast<long long>(b) * a.bt_stride;
+  if (a.dst.block_table != a.src.block_table)
+    for (int i = tid; i < r.n; i += nt) a.dst.block_table[row + i] = a.src.block_table[row + i];
+  if (a.dst.block_pos && a.dst.block_pos != a.src.block_pos)
+    for (int i = tid; i < r.n; i += nt) a.dst.block_pos[row + i] = a.src.block_pos[row + i];
+  if (a.dst.score != a.src.score)
+    for (int i = tid; i < r.n; i += nt) a.dst.score[row + i] = a.src.score[row + i];
+  return false;
+}
 
-__global__ void __launch_bounds__(1024) evict_kernel(const __grid_constant__ EvictArgs a) {
+// A CTA per sequence, the whole row's scores in registers (PER a thread, entry tid + i * nt; NaN
+// in place of what is not a middle entry, so that no comparison counts it).
+//
+// Threshold: the (budget - sink - recent)-th largest score, by its key T, bit by bit from the
+// first bit in which the keys differ; each bit is one comparison per score and one count over
+// the block, and the search ends early when a candidate keeps exactly as many as wanted, or
+// before it begins when the smallest score is the threshold (pages that were never attended).
+// Placement: per (chunk of nt entries, warp) counts of the kept entries, one scan of them, then
+// kept entries go to the front and freed pages onto the stack, four chunks at a time. Chunks
+// are read before any of them is written, and entries only move towards the front, so dst may
+// be src.
+// Bound by the latency of some 15 block-wide counts and of the three arrays, and, for rows of
+// thousands, by the instructions of the one SM that holds the row.
+template <int PER, int MAXT>
+__global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ EvictArgs a) {
+  static_assert(PER <= 32, "a bit per entry, a thread per (chunk, warp)");
+  __shared__ EvictShared sh;
+  __shared__ int place[PER * (MAXT / 32)];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nt = blockDim.x, nwarps = nt >> 5;
+  const long long row = static_cast<long long>(b) * a.bt_stride;
+  EvictRow r;
+  if (!evict_begin(a, b, tid, nt, r)) return;
+  const int32_t* table = a.src.block_table + row;
+  const int32_t* bpos = a.src.block_pos ? a.src.block_pos + row : nullptr;
+  const float* score = a.src.score + row;
+  const int n = r.n, m0 = a.n_sink, m1 = n - a.n_recent;   // the middle entries: [m0, m1)
+  const int want = a.budget - a.n_sink - a.n_recent;       // of them are kept: 0 <= want < m1 - m0
+  const float none = __int_as_float(0x7fffffff);
+  float s[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid + i * nt;
+    s[i] = none;
+    if (i * nt < m1 && e >= m0 && e < m1) s[i] = score[e];
+  }
+  int which = 0;
+  // How a score is judged: kept where it is above f (or also where equal, if `geq`); of the
+  // scores equal to f, or, with nan_ties, of the NaN ones, the first `ties` by index.
+  float f = INFINITY;
+  bool geq = false, nan_ties = false;
+  int ties = 0;
+  if (want > 0) {
+    float lo = INFINITY, hi = -INFINITY;
+    int real = 0;                                          // scores that are numbers
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      lo = fminf(lo, s[i]);
+      hi = fmaxf(hi, s[i]);
+      real += s[i] == s[i];
+    }
+    uint32_t klo = __reduce_min_sync(0xffffffffu, score_key(lo));
+    uint32_t khi = __reduce_max_sync(0xffffffffu, score_key(hi));
+    real = __reduce_add_sync(0xffffffffu, real);
+    if (nwarps > 1) {
+      if (lane == 0) {
+        sh.cnt[0][warp] = static_cast<int>(klo);
+        sh.cnt[1][warp] = static_cast<int>(khi);
+        sh.cnt2[warp] = real;
+      }
+      __syncthreads();
+      klo = __reduce_min_sync(0xffffffffu, lane < nwarps ? static_cast<uint32_t>(sh.cnt[0][lane]) : 0xffffffffu);
+      khi = __reduce_max_sync(0xffffffffu, lane < nwarps ? static_cast<uint32_t>(sh.cnt[1][lane]) : 0u);
+      real = __reduce_add_sync(0xffffffffu, lane < nwarps ? sh.cnt2[lane] : 0);
+      __syncthreads();
+    }
+    if (real <= want) {                                    // all numbers stay, and the first NaNs
+      f = -INFINITY;
+      geq = true;
+      nan_ties = true;
+      ties = want - real;
+    } else {
+      f = key_score(klo);
+      int above = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) above += s[i] > f;
+      above = block_sum(above, &sh, which, warp, lane, nwarps);
+      ties = want - above;                                 // > 0: the smallest score is the threshold
+      if (above == want) {
+        ties = 0;
+      } else if (above > want) {
+        int bit = 31 - __clz(klo ^ khi);                   // all keys share the bits above
+        uint32_t T = bit == 31 ? 0u : klo & ~((2u << bit) - 1u);
+        int c = real;
+        for (; bit >= 0 && c != want; --bit) {
+          const uint32_t cand = T | (1u << bit);
+          f = key_score(cand);
+          int k = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) k += s[i] >= f;
+          k = block_sum(k, &sh, which, warp, lane, nwarps);
+          if (k >= want) {
+            T = cand;
+            c = k;
+          }
+        }
+        f = key_score(T);
+        if (c == want) {
+          geq = true;
+          ties = 0;
+        } else {
+          above = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) above += s[i] > f;
+          ties = want - block_sum(above, &sh, which, warp, lane, nwarps);
+        }
+      }
+    }
+  }
+  // which entries stay: bit i for entry tid + i * nt
+  uint32_t keep = 0;
+  int tied = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (i * nt >= n) continue;
+    const int e = tid + i * nt;
+    const bool mid = e >= m0 && e < m1;
+    bool stay = s[i] > f || (geq && s[i] == f) || (e < n && !mid);
+    if (tied < ties) {                                     // (uniform: there are ties left to place)
+      const bool tie = mid && (nan_ties ? s[i] != s[i] : s[i] == f);
+      const unsigned mask = __ballot_sync(0xffffffffu, tie);
+      __syncthreads();
+      if (lane == 0) sh.cnt2[warp] = __popc(mask);
+      __syncthreads();
+      const int tw = lane < nwarps ? sh.cnt2[lane] : 0;
+      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? tw : 0);
+      if (tie && tied + before + __popc(mask & ((1u << lane) - 1u)) < ties) stay = true;
+      tied += __reduce_add_sync(0xffffffffu, tw);
+    }
+    keep |= static_cast<uint32_t>(stay) << i;
+    const unsigned mask = __ballot_sync(0xffffffffu, stay);
+    if (lane == 0) place[i * nwarps + warp] = __popc(mask);
+  }
+  __syncthreads();
+  // exclusive scan of the counts, a thread each
+  const int cells = (n + nt - 1) / nt * nwarps;
+  const int v = tid < cells ? place[tid] : 0;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) sh.cnt2[warp] = incl;
+  __syncthreads();
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.cnt2[lane] : 0);
+  if (tid < cells) place[tid] = before + incl - v;
+  __syncthreads();
+  int32_t* o_table = a.dst.block_table + row;
+  int32_t* o_pos = a.dst.block_pos ? a.dst.block_pos + row : nullptr;
+  float* o_score = a.dst.score + row;
+  int32_t* push = a.dst.free_list + static_cast<long long>(b) * a.free_stride + r.have;
+  constexpr int STEP = 4;
+  static_assert(PER % STEP == 0, "chunks");
+  int page[STEP], pos[STEP];
+  float sc[STEP];
+#pragma unroll
+  for (int i0 = 0; i0 < PER; i0 += STEP) {
+    if (i0 * nt >= n) break;
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+      const int e = tid + (i0 + i) * nt;
+      const bool stay = (keep >> (i0 + i)) & 1u;           // positions and scores go with kept entries only
+      page[i] = e < n ? table[e] : 0;
+      pos[i] = stay && bpos ? bpos[e] : 0;
+      sc[i] = stay ? score[e] : 0.f;
+    }
+    __syncthreads();                     // these chunks are read
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+      const int e = tid + (i0 + i) * nt;
+      const bool stay = (keep >> (i0 + i)) & 1u;
+      const unsigned mask = __ballot_sync(0xffffffffu, stay);
+      if (e < n) {
+        const int to = place[(i0 + i) * nwarps + warp] + __popc(mask & ((1u << lane) - 1u));
+        if (stay) {
+          o_table[to] = page[i];
+          if (o_pos) o_pos[to] = pos[i];
+          o_score[to] = sc[i];
+        } else {
+          push[e - to] = page[i];        // entries freed before this one
+        }
+      }
+    }
+  }
+}
+
+// Rows longer than the registers hold: the same search over keys read again for each bit, and
+// the placement a chunk of nt entries at a time.
+__global__ void __launch_bounds__(1024) evict_long_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ EvictShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = blockDim.x, nwarps = nt >> 5;
   const long long row = static_cast<long long>(b) * a.bt_stride;
+  EvictRow r;
+  if (!evict_begin(a, b, tid, nt, r)) return;
   const int32_t* table = a.src.block_table + row;
   const int32_t* bpos = a.src.block_pos ? a.src.block_pos + row : nullptr;
   const float* score = a.src.score + row;
   int32_t* o_table = a.dst.block_table + row;
   int32_t* o_pos = a.dst.block_pos ? a.dst.block_pos + row : nullptr;
   float* o_score = a.dst.score + row;
-  const int n = a.src.n_entries[b];
-  const int have = a.src.free_cnt[b];
-  const int tail = a.src.tail_len[b];
-  __syncthreads();                          // the counts are read before any thread writes them
-  int bits = 0;
-  if (n < 0 || n > a.bt_stride || have < 0 || have > a.free_stride) bits = LSA_DEVERR_BAD_SIZE;
-  int gone = bits == 0 && n > a.budget ? n - a.budget : 0;
-  if (gone > 0 && gone > a.free_stride - have) {
-    bits = LSA_DEVERR_POOL_CAPACITY;
-    gone = 0;
-  }
-  if (tid == 0) {
-    a.dst.n_entries[b] = n - gone;
-    a.dst.free_cnt[b] = have + gone;
-    a.dst.tail_len[b] = tail;
-    if (bits) set_err(a.err, bits);
-  }
-  if (bits == LSA_DEVERR_BAD_SIZE) return;
-  if (gone == 0) {
-    if (a.dst.block_table != a.src.block_table)
-      for (int i = tid; i < n; i += nt) o_table[i] = table[i];
-    if (o_pos && a.dst.block_pos != a.src.block_pos)
-      for (int i = tid; i < n; i += nt) o_pos[i] = bpos[i];
-    if (a.dst.score != a.src.score)
-      for (int i = tid; i < n; i += nt) o_score[i] = score[i];
-    return;
-  }
-  const int m0 = a.n_sink, m1 = n - a.n_recent;          // the middle entries
-  const int want = a.budget - a.n_sink - a.n_recent;     // of them are kept: 0 <= want < m1 - m0
-  uint32_t T = 0xffffffffu;                              // keys above T stay,
-  int ties = 0;                                          //   and the first `ties` of those equal to it
+  const int n = r.n, m0 = a.n_sink, m1 = n - a.n_recent;
+  const int want = a.budget - a.n_sink - a.n_recent;
+  uint32_t T = 0xffffffffu;
+  int ties = 0, which = 0;
   if (want > 0) {
-    uint32_t key[PER];
-    const bool in_regs = m1 - m0 <= PER * nt;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = m0 + tid + i * nt;
-      key[i] = in_regs && e < m1 ? score_key(score[e]) : 0u;
-    }
     T = 0u;
-    int which = 0;
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t cand = T | (1u << bit);
       int c = 0;
-      if (in_regs) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) c += key[i] >= cand;   // cand >= 1: the padding 0 never counts
-      } else {
-        for (int e = m0 + tid; e < m1; e += nt) c += score_key(score[e]) >= cand;
-      }
+      for (int e = m0 + tid; e < m1; e += nt) c += score_key(score[e]) >= cand;
       c = block_sum(c, &sh, which, warp, lane, nwarps);
-      which ^= 1;
       if (c >= want) T = cand;
     }
     int above = 0;
-    if (in_regs) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) above += key[i] > T;
-    } else {
-      for (int e = m0 + tid; e < m1; e += nt) above += score_key(score[e]) > T;
-    }
-    above = block_sum(above, &sh, which, warp, lane, nwarps);
-    ties = want - above;
+    for (int e = m0 + tid; e < m1; e += nt) above += score_key(score[e]) > T;
+    ties = want - block_sum(above, &sh, which, warp, lane, nwarps);
   }
-  // placement, a chunk of nt entries at a time
-  int32_t* push = a.dst.free_list + static_cast<long long>(b) * a.free_stride + have;
+  int32_t* push = a.dst.free_list + static_cast<long long>(b) * a.free_stride + r.have;
   int kept = 0, tied = 0;                                // so far, in earlier chunks
   for (int c0 = 0; c0 < n; c0 += nt) {
     const int e = c0 + tid;
@@ -417,8 +598,16 @@ extern "C" lsa_status lsa_paged_evict(const lsa_paged_cache* c, int32_t budget, 
   a.budget = budget;
   a.n_sink = n_sink;
   a.n_recent = n_recent;
-  // up to 4 entries a thread while that keeps the block small: barriers cost more than loads
-  const int want = (c->bt_stride + 3) / 4;
-  const unsigned threads = want > 512 ? 1024 : want > 256 ? 512 : want > 128 ? 256 : want > 64 ? 128 : want > 32 ? 64 : 32;
-  return launch(lsa::paged_tables::evict_kernel, a, static_cast<unsigned>(c->B), threads, stream);
+  // Up to 8 scores a thread: a warp alone needs no barriers for rows of up to 256 entries (65
+  // entries: 1 warp X us, 3 warps Y us), then blocks of up to 512. Longer rows take 24 a thread,
+  // and rows that do not fit the registers of a block are read again for each bit.
+  const int stride = c->bt_stride;
+  const unsigned B = static_cast<unsigned>(c->B);
+  if (stride <= 8 * 512) {
+    const unsigned threads = stride <= 256 ? 32 : (stride + 255) / 256 * 32;
+    return launch(lsa::paged_tables::evict_kernel<8, 512>, a, B, threads, stream);
+  }
+  if (stride <= 24 * 768)
+    return launch(lsa::paged_tables::evict_kernel<24, 768>, a, B, (stride + 767) / 768 * 32, stream);
+  return launch(lsa::paged_tables::evict_long_kernel, a, B, 1024, stream);
 }
