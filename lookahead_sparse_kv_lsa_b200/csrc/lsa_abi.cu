@@ -85,18 +85,26 @@ lsa_status encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t inner, u
   return r == CUDA_SUCCESS ? LSA_OK : LSA_ERR_CUDA;
 }
 
-lsa_status encode_tiled_rows(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows,
-                             uint32_t box_rows) {
+static lsa_status encode_3d(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[3],
+                            const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3]) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return LSA_ERR_CUDA;
-  const cuuint64_t dims[3] = {64, rows, d / 64};
-  const cuuint64_t strides[2] = {d * 2, 128};
-  const cuuint32_t box[3] = {64, box_rows, static_cast<cuuint32_t>(d / 64)};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? LSA_OK : LSA_ERR_CUDA;
+}
+
+lsa_status encode_tiled_rows(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows,
+                             uint32_t box_rows) {
+  return encode_3d(map, base, {64, rows, d / 64}, {d * 2, 128},
+                   {64, box_rows, static_cast<cuuint32_t>(d / 64)});
+}
+
+lsa_status encode_tiled_planes(CUtensorMap* map, const void* base, uint64_t d, uint32_t rows,
+                               uint64_t planes) {
+  return encode_3d(map, base, {d, rows, planes}, {d * 2, d * 2 * rows}, {64, rows, 1});
 }
 
 }  // namespace lsa_host

@@ -145,6 +145,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int32_t x, int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -423,6 +432,11 @@ lsa_status encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t inner, u
 // rows as d/64 adjacent tiles of [box_rows][64] with the 128-byte swizzle (coordinates 0, row, 0).
 lsa_status encode_tiled_rows(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows,
                              uint32_t box_rows);
+
+// Map of 16-bit planes [planes][rows][d]: one copy brings 64 elements of `rows` rows of a plane
+// with the 128-byte swizzle, from any row on; rows outside the plane come as zeros.
+lsa_status encode_tiled_planes(CUtensorMap* map, const void* base, uint64_t d, uint32_t rows,
+                               uint64_t planes);
 
 // Fused token append for the decode-step path: k_new / v_new [B][d] go into slot
 // tail-1 of each sequence's last block-table page; tail_len_out receives `tail`.

@@ -36,8 +36,12 @@
 // P is written token-major ([128 tokens][heads], 16-byte stores) and read by the tensor cores
 // as an MN-major operand, swizzled by its row size.
 //
-// Rows that are not seen get weight 0, and in a tile that has any, the softmax warps clear
-// their rows of V in shared memory before the product reads them: 0 * NaN would be NaN.
+// Rows that are not seen get weight 0, and their values must be 0 too: 0 * NaN would be NaN. A
+// page is loaded by a box of 64 rows that starts at a row of its own (its shift): a page
+// whose first k slots are seen (the tail page, the end of the prefix) from row k - 64, a page
+// whose first k are not (the start of the window) from row k. What lies outside the page
+// comes as zeros and is not read. Only a page with both, seen slots between or around ones
+// that are not, is loaded whole, and the softmax warps clear these rows in shared memory.
 #include "lsa_common.cuh"
 
 #include <math.h>
@@ -51,7 +55,7 @@ constexpr int TILE = 128;                 // tokens per tile, two pages: the MMA
 constexpr int STAGE_BYTES = TILE * 128;   // [128 rows][64 dims] 16-bit = 16 KB
 constexpr int NTHREADS = 192;
 constexpr int MAXREC = 32;                // sequences a CTA plans at a time
-constexpr int YRING = 128;                // pages whose pool rows the producer has looked up
+constexpr int YRING = 128;                // pages that the producer has looked up
 constexpr float RESCALE_LOG2 = 8.0f;      // raise the running max only by more than 2^8
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int JOIN_THREADS = 256;
@@ -67,6 +71,8 @@ struct Rec {
   int n, tail;       // entries, tokens in the last one
   int e1, e2;        // seen entries: [0, e1) and [e2, n)
   int masked;        // whether low / pre exclude any position of a seen entry
+  int shift_pre, shift_low, shift_last;   // shifts of the seen pages e1 - 1, e1 and the last one
+  int dirty;         // the seen page that needs its rows cleared, -1: none
 };
 
 // The split: the cost positions from `off` on over `ctas` CTAs, the first `rem` of them with
@@ -171,10 +177,13 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
   r.low = 0;
   r.pre = 0;
   r.pages = r.n = r.tail = r.e1 = r.e2 = r.masked = 0;
+  r.shift_pre = r.shift_low = r.shift_last = 0;
+  r.dirty = -1;
   bad = n != 0 && (n < 0 || n > a.bt_stride || tail < 1 || tail > PAGE);
   if (n == 0 || bad) return r;
   r.n = n;
   r.tail = tail;
+  r.shift_last = tail - PAGE;
   const bool masks = doc > 0 || a.window > 0;
   if (masks || a.slopes != nullptr) {
     const int32_t* pos = a.block_pos ? a.block_pos + static_cast<long long>(b) * a.bt_stride : nullptr;
@@ -188,7 +197,26 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
       r.pre = pre < 0 ? 0 : pre;
       r.e2 = first_at_least(pos, n, first, last, low >> 6);   // its last position >= low
       if (r.pre > 0) r.e1 = first_at_least(pos, n, first, last, (static_cast<long long>(r.pre) + PAGE - 1) >> 6);
-      if (r.e1 > r.e2) r.e1 = r.e2;                           // one entry holds both bounds
+      const bool hole = r.e1 > r.e2;                          // one entry holds both bounds
+      if (hole) r.e1 = r.e2;
+      // slots before the window in its first entry, slots of the prefix in its last
+      const int k_low = r.e2 < n ? static_cast<int>(max(0ll, low - (pos ? pos[r.e2] : r.e2) * static_cast<long long>(PAGE))) : 0;
+      const int k_pre = r.e1 > 0 ? static_cast<int>(min(static_cast<long long>(PAGE), r.pre - (pos ? pos[r.e1 - 1] : r.e1 - 1) *
+                                                                                          static_cast<long long>(PAGE))) : PAGE;
+      r.shift_pre = k_pre - PAGE;
+      if (hole) {
+        r.dirty = r.e1;
+      } else {
+        r.shift_low = k_low;
+      }
+      if (r.e1 == n) {                                        // all seen entries are the prefix's
+        r.shift_last = min(k_pre, tail) - PAGE;
+      } else if (r.e2 == n) {                                 // the tail page is not seen
+        r.shift_last = r.shift_pre;
+      } else if (r.e2 == n - 1 && (hole || k_low > 0)) {      // the window starts in the tail page
+        r.shift_last = hole || tail < PAGE ? 0 : k_low;
+        if (tail < PAGE) r.dirty = r.e1;
+      }
     }
     const int j = r.e2 < n ? n - 1 : r.e1 - 1;                // last seen entry
     r.ref = (j == n - 1 || !pos ? (pos ? last : j) : pos[j < 0 ? 0 : j]) * static_cast<long long>(PAGE) + PAGE - 1;
@@ -242,11 +270,17 @@ __device__ __forceinline__ void tile_pages(const Seg& s, int t, int& t0, int& t1
   t0 = t == 0 ? s.u1 - first : t1 - 2;
 }
 
-// Whether a tile may hold rows that are loaded but not seen: the end of the tail page and
-// the entries at the masks' bounds. Every role gives the same answer.
-__device__ __forceinline__ bool tile_dirty(const Rec& r, int t0, int t1) {
-  if (t1 == r.pages && r.tail < PAGE && (r.e2 < r.n || r.e1 == r.n)) return true;
-  return r.masked && t1 > r.e1 - 1 && t0 < r.e1 + 1;
+// Row of a seen page that its box starts at.
+__device__ __forceinline__ int page_shift(const Rec& r, int u) {
+  return u == r.pages - 1 ? r.shift_last : u == r.e1 - 1 ? r.shift_pre : u == r.e1 ? r.shift_low : 0;
+}
+
+// Whether a tile holds rows that are loaded but not seen. Every role gives the same answer.
+__device__ __forceinline__ bool tile_dirty(const Rec& r, int t0, int t1) { return r.dirty >= t0 && r.dirty < t1; }
+
+// Whether the newest token sees slot `in_page`, at position x, of a seen entry.
+__device__ __forceinline__ bool slot_seen(const Rec& r, int entry, int in_page, long long x) {
+  return in_page >= 0 && in_page < (entry == r.n - 1 ? r.tail : PAGE) && (!r.masked || x < r.pre || x >= r.low);
 }
 
 template <int HP>
@@ -262,7 +296,7 @@ struct Misc {
   Split split;
   int2 wsum[NTHREADS / 32];
   Rec rec[MAXREC];
-  int y[YRING];
+  int plane[YRING];                // K planes of the pages looked up, -1: outside the pool
   float red[4][HP];
   __align__(16) float m[HP];       // running max per head (log2 units), 0 while nothing was seen
   __align__(16) float over[HP];    // running max + RESCALE_LOG2, -inf while nothing was seen
@@ -607,8 +641,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       const uint64_t evict_first = l2_policy_evict_first();
-      const int y_out = static_cast<int>(a.n_pages * 2 * a.Hkv * PAGE);   // outside the map
-      const int kv_rows = a.Hkv * PAGE;
+      const int outside = static_cast<int>(a.n_pages * 2 * a.Hkv);   // a plane outside the map
       bool ok = true;
       for (int ri = 0; ri < nrec && ok; ++ri) {
         const Rec& r = m->rec[ri];
@@ -634,19 +667,19 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             int t0, t1;
             tile_pages(sg, i, t0, t1);
             if (i < T && sg.u1 - t0 > filled) {
-              // the pool rows of the next 64 pages, by all lanes
+              // the pool planes of the next 64 pages, by all lanes
               __syncwarp();
 #pragma unroll
               for (int e = 0; e < YRING / 64; ++e) {
                 const int k = filled + 32 * e + lane;
                 if (k < len) {
                   const int page = bt[page_entry(r, sg.u1 - 1 - k)];
-                  int y = -1;
+                  int plane = -1;
                   if (page < 0 || page >= a.n_pages)
                     set_err(a.err, LSA_DEVERR_BAD_PAGE);
                   else
-                    y = (page * 2 * a.Hkv + sg.kvh) * PAGE;
-                  m->y[k & (YRING - 1)] = y;
+                    plane = page * 2 * a.Hkv + sg.kvh;
+                  m->plane[k & (YRING - 1)] = plane;
                 }
               }
               filled += YRING / 2;
@@ -658,14 +691,15 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                 const int tile = kv == 0 ? i : i - 1;
                 if (tile < 0 || tile >= T) continue;
                 tile_pages(sg, tile, t0, t1);
-                int ys[2];
+                int zs[2], ys[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                   // rows past the tile's pages and bad pages: a box outside the map, which
                   // the copy engine fills with zeros without reading memory
                   const int u = t0 + x;
-                  const int y = u < t1 ? m->y[(sg.u1 - 1 - u) & (YRING - 1)] : -1;
-                  ys[x] = y < 0 ? y_out : y + kv * kv_rows;
+                  const int plane = u < t1 ? m->plane[(sg.u1 - 1 - u) & (YRING - 1)] : -1;
+                  zs[x] = plane < 0 ? outside : plane + kv * a.Hkv;
+                  ys[x] = page_shift(r, u);
                 }
                 for (int c = 0; c < NDC; ++c) {
                   const int st = ring_pos % NST;
@@ -675,7 +709,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                   uint8_t* dst = sRing + st * STAGE_BYTES;
 #pragma unroll
                   for (int x = 0; x < 2; ++x)
-                    tma_load_2d_hint(dst + x * (PAGE * 128), &map_kv, &m->full[st], 64 * c, ys[x],
+                    tma_load_3d_hint(dst + x * (PAGE * 128), &map_kv, &m->full[st], 64 * c, ys[x], zs[x],
                                      evict_first);
                   ++ring_pos;
                 }
@@ -823,7 +857,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             tile_pages(sg, j, t0, t1);
             const bool dirty = tile_dirty(r, t0, t1);
             const int u = t0 + (sw >> 1);
-            const int in_page = (sw & 1) * HALF + lane;
+            const int in_page = (sw & 1) * HALF + lane + page_shift(r, u);
             const int page = page_n;
             const long long x0 = static_cast<long long>(pos_n) * PAGE + in_page;
             if (j + 1 < T) {
@@ -833,10 +867,8 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
               page_n = bt[e];
               pos_n = bp ? bp[e] : e;
             }
-            bool seen = u < t1 && page >= 0 && page < a.n_pages;
             const int entry = u < t1 ? page_entry(r, u) : 0;
-            if (seen && entry == r.n - 1) seen = in_page < r.tail;
-            if (seen && r.masked) seen = x0 < r.pre || x0 >= r.low;
+            const bool seen = u < t1 && page >= 0 && page < a.n_pages && slot_seen(r, entry, in_page, x0);
             const bool all_seen = __all_sync(0xffffffffu, seen);
             const int sb = gtile_s & 1;
             if (!failed)
@@ -1506,9 +1538,7 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   const int G = c->H / c->Hkv;
 
   CUtensorMap mkv, mq;
-  st = lsa_host::encode_tiled_2d(&mkv, c->pool, c->d, static_cast<uint64_t>(c->n_pages) * 2 * c->Hkv * LSA_BLOCK,
-                                 static_cast<uint64_t>(c->d) * 2, 64, lsa::paged::PAGE,
-                                 CU_TENSOR_MAP_SWIZZLE_128B);
+  st = lsa_host::encode_tiled_planes(&mkv, c->pool, c->d, LSA_BLOCK, static_cast<uint64_t>(c->n_pages) * 2 * c->Hkv);
   if (st != LSA_OK) return st;
   const int HP = G <= 16 ? 16 : G <= 32 ? 32 : 64;
   st = lsa_host::encode_tiled_rows(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H, HP);

@@ -229,6 +229,9 @@ MASKS = [
     dict(docs=[10 ** 6] * 4), dict(docs=[10 ** 6] * 4, prefix=[0, 1, 70, 500]),
     dict(docs=[599, 598, 560, 575], prefix=[0, 577, 577, 5]), dict(docs=[300, 10, 130, 64], window=256),
     dict(prefix=[-5, 0, 10 ** 6, 2], docs=[-7, 3, 4, 5], window=3),
+    # both bounds in one page: slots are missing in its middle
+    dict(docs=[100, 90, 127, 40], prefix=[70, 65, 66, 10]), dict(docs=[599, 590, 576, 63], prefix=[598, 577, 570, 3]),
+    dict(window=30), dict(docs=[590, 580, 570, 20], prefix=[500, 576, 540, 0]),
 ]
 
 
