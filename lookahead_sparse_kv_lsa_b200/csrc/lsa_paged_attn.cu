@@ -27,7 +27,8 @@
 //   warp 1    tcgen05.mma: S^T[token][head] = K Q^T (M = 128, N = heads padded to 16, 32 or
 //             64), double buffered in TMEM; O^T[dim][head] += V^T P (M = 128 dims, K = 128
 //             tokens), accumulated in TMEM;
-//   warps 2-5 softmax, one token row per thread: the row's scores stay in registers from the
+//   warps 2-.. softmax, a token row (of up to 32 heads: 64 heads take two groups of four
+//             warps) per thread: the row's scores stay in registers from the
 //             one TMEM load to the rounding of P. A vote (one barrier with reduction) finds
 //             whether any score exceeds its head's running max by more than 2^8; only then is
 //             the tile max formed and O^T rescaled. Each half page's per-head sums (a butterfly
@@ -53,7 +54,6 @@ constexpr int PAGE = LSA_BLOCK;
 constexpr int HALF = 32;                  // rows of a softmax warp: half a page
 constexpr int TILE = 128;                 // tokens per tile, two pages: the MMA M of S^T
 constexpr int STAGE_BYTES = TILE * 128;   // [128 rows][64 dims] 16-bit = 16 KB
-constexpr int NTHREADS = 192;
 constexpr int MAXREC = 32;                // sequences a CTA plans at a time
 constexpr int YRING = 128;                // pages that the producer has looked up
 constexpr float RESCALE_LOG2 = 8.0f;      // raise the running max only by more than 2^8
@@ -283,6 +283,17 @@ __device__ __forceinline__ bool slot_seen(const Rec& r, int entry, int in_page, 
   return in_page >= 0 && in_page < (entry == r.n - 1 ? r.tail : PAGE) && (!r.masked || x < r.pre || x >= r.low);
 }
 
+// Heads per softmax thread, groups of four softmax warps, threads. Two groups halve the time from
+// scores to weights and the epilogue of 64 heads; for 32 heads they would not leave enough
+// registers for two CTAs per SM.
+template <int HP>
+struct Roles {
+  static constexpr int HW = HP < 32 ? HP : 32;
+  static constexpr int GROUPS = HP / HW;
+  static constexpr int SOFT = 128 * GROUPS;
+  static constexpr int NT = 64 + SOFT;
+};
+
 template <int HP>
 struct Misc {
   uint64_t full[8], empty[8];
@@ -294,7 +305,7 @@ struct Misc {
   int nrec, more, rank0, rank1;
   int cs, ce;                      // the CTA's cost range
   Split split;
-  int2 wsum[NTHREADS / 32];
+  int2 wsum[Roles<HP>::NT / 32];
   Rec rec[MAXREC];
   int plane[YRING];                // K planes of the pages looked up, -1: outside the pool
   float red[4][HP];
@@ -322,7 +333,7 @@ __device__ __forceinline__ int2 block_scan(int cost, bool flag, Misc<HP>* m, int
   int2 pre = make_int2(incl - cost, __popc(mask & ((1u << lane) - 1u)));
   tot = make_int2(0, 0);
 #pragma unroll
-  for (int w = 0; w < NTHREADS / 32; ++w) {
+  for (int w = 0; w < Roles<HP>::NT / 32; ++w) {
     const int2 t = m->wsum[w];
     if (w < warp) {
       pre.x += t.x;
@@ -372,6 +383,7 @@ __device__ __forceinline__ void write_plan(const Args& a, const Rec& r, bool bad
 // the plan is straight-line code that runs once, and fetching it costs more than running it.
 template <int HP>
 __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int skip, Misc<HP>* m, int tid) {
+  constexpr int NT = Roles<HP>::NT;
   const int lane = tid & 31;
   const int cta = blockIdx.x;
   const bool write = cta == 0 && skip == 0 && !dry;
@@ -408,14 +420,14 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
     __syncthreads();
     return;
   }
-  const bool one = B <= NTHREADS;                     // one sequence per thread: read it once
+  const bool one = B <= NT;                           // one sequence per thread: read it once
   int2 pre = make_int2(0, 0), tot;
   if (one) {
     if (tid < B) r = read_seq(a, tid, bad);
     pre = block_scan(cost_of(a, r.pages), r.pages > 0, m, tid, tot);
   } else {
     int mine = 0, seqs = 0;
-    for (int b = tid; b < B; b += NTHREADS) {
+    for (int b = tid; b < B; b += NT) {
       const int pages = read_seq(a, b, bad).pages;
       mine += cost_of(a, pages);
       seqs += pages > 0;
@@ -435,7 +447,7 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
     m->split = sp;
   }
   int2 base = make_int2(0, 0);
-  for (int b0 = 0; b0 < B; b0 += NTHREADS) {
+  for (int b0 = 0; b0 < B; b0 += NT) {
     const int b = b0 + tid;
     if (!one) {
       r.pages = 0;
@@ -468,7 +480,7 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
 }
 
 // Fixed cost of a segment in pages, and the least share of pages that a CTA is started for.
-__host__ __device__ constexpr int overhead_pages(int d) { return d >= 256 ? 6 : 8; }
+__host__ __device__ constexpr int overhead_pages(int) { return 5; }
 __host__ __device__ constexpr int least_pages(int d) { return d >= 256 ? 1 : 2; }
 
 // Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
@@ -579,7 +591,7 @@ __device__ __forceinline__ float4 quad_transpose(float v0, float v1, float v2, f
 }
 
 template <int HP, int NDC>
-__global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
+__global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
     paged_attn_kernel(const __grid_constant__ CUtensorMap map_kv,
                       const __grid_constant__ CUtensorMap map_q, const __grid_constant__ Args a) {
   using LY = Layout<HP, NDC>;
@@ -601,9 +613,9 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m->s_full[i], 1);
-      mbar_init(&m->s_free[i], 4);   // one arrival per softmax warp
+      mbar_init(&m->s_free[i], 4 * Roles<HP>::GROUPS);   // one arrival per softmax warp
     }
-    mbar_init(&m->p_full, 4);
+    mbar_init(&m->p_full, 4 * Roles<HP>::GROUPS);
     mbar_init(&m->pv_done, 1);
     mbar_init(&m->q_full, 1);
     mbar_init(&m->q_free, 1);
@@ -701,6 +713,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                   zs[x] = plane < 0 ? outside : plane + kv * a.Hkv;
                   ys[x] = page_shift(r, u);
                 }
+#pragma unroll 1
                 for (int c = 0; c < NDC; ++c) {
                   const int st = ring_pos % NST;
                   ok = mbar_wait(&m->empty[st], ((ring_pos / NST) & 1) ^ 1, abort);
@@ -810,17 +823,20 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
       }
     } else {
       // ---------------------------------------------------------------- softmax
-      // Every wait result is folded into the next barrier with reduction, so the four warps
-      // leave together and no named barrier is left half-arrived.
+      // Every wait result is folded into the next barrier with reduction, so the warps leave
+      // together and no named barrier is left half-arrived.
       const int sw = warp & 3;                   // TMEM lanes, and half page of the tile, of this warp
-      const int t128 = tid - 64;
+      constexpr int HW = Roles<HP>::HW, SOFT = Roles<HP>::SOFT;
+      const int hg = (warp - 2) >> 2;            // group: heads [hb, hb + HW)
+      const int hb = hg * HW;
+      const int ts = tid - 64;
       const uint32_t row = sw * 32 + lane;       // token row of the tile
       const uint32_t lane_addr = static_cast<uint32_t>(sw * 32) << 16;
       const bool f16 = a.f16 != 0;
       const float scale2 = a.cap > 0.f ? a.scale / a.cap : a.scale * LOG2E;
       const float cap2 = a.cap * LOG2E;
-      constexpr int HL = HP >= 32 ? HP / 32 : 1;  // heads whose sums a lane holds
-      const int h_lane = HP >= 32 ? lane * HL : lane >> 1;
+      constexpr int HL = HW >= 32 ? HW / 32 : 1;  // heads whose sums a lane holds, from h_lane on
+      const int h_lane = hb + (HW >= 32 ? lane * HL : lane >> 1);
       bool failed = false;
       for (int ri = 0; ri < nrec && !failed; ++ri) {
         const Rec& r = m->rec[ri];
@@ -834,11 +850,11 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
         while (!failed && walk.next(r, sg)) {
           const int T = seg_tiles(sg);
           const int h0 = sg.kvh * G;
-          if (t128 < HP) {
-            m->m[t128] = 0.f;
-            m->m_raw[t128] = -INFINITY;
-            m->over[t128] = -INFINITY;
-            m->slope[t128] = a.slopes != nullptr && t128 < G ? a.slopes[h0 + t128] * LOG2E : 0.f;
+          if (ts < HP) {
+            m->m[ts] = 0.f;
+            m->m_raw[ts] = -INFINITY;
+            m->over[ts] = -INFINITY;
+            m->slope[ts] = a.slopes != nullptr && ts < G ? a.slopes[h0 + ts] * LOG2E : 0.f;
           }
           float l[HL];
 #pragma unroll
@@ -852,7 +868,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             page_n = bt[e];
             pos_n = bp ? bp[e] : e;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1, SOFT);
           for (int j = 0; j < T; ++j) {
             tile_pages(sg, j, t0, t1);
             const bool dirty = tile_dirty(r, t0, t1);
@@ -874,28 +890,28 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             if (!failed)
               failed = !__all_sync(0xffffffffu, mbar_wait(&m->s_full[sb], (gtile_s >> 1) & 1, abort));
             tc_fence_after();
-            float x[HP];
+            float x[HW];
             bool over = false;
             if (!failed) {
-              tmem_ld_row<HP>(tmem + lane_addr + sb * HP, x);
+              tmem_ld_row<HW>(tmem + lane_addr + sb * HP + hb, x);
               tmem_wait_ld();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&m->s_free[sb]);
               if (a.cap > 0.f) {
                 if (cap2 <= SMALL_CAP)
-                  cap_scores<HP, false>(x, scale2, cap2);
+                  cap_scores<HW, false>(x, scale2, cap2);
                 else
-                  cap_scores<HP, true>(x, scale2, cap2);
+                  cap_scores<HW, true>(x, scale2, cap2);
               } else {
 #pragma unroll
-                for (int h = 0; h < HP; ++h) x[h] *= scale2;
+                for (int h = 0; h < HW; ++h) x[h] *= scale2;
               }
               if (a.slopes != nullptr) {
                 const float rel = static_cast<float>(x0 - r.ref);
 #pragma unroll
-                for (int h = 0; h < HP; h += 4) {
-                  const float4 s = *reinterpret_cast<const float4*>(m->slope + h);
+                for (int h = 0; h < HW; h += 4) {
+                  const float4 s = *reinterpret_cast<const float4*>(m->slope + hb + h);
                   x[h] = fmaf(s.x, rel, x[h]);
                   x[h + 1] = fmaf(s.y, rel, x[h + 1]);
                   x[h + 2] = fmaf(s.z, rel, x[h + 2]);
@@ -904,12 +920,12 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
               }
               if (!all_seen) {
 #pragma unroll
-                for (int h = 0; h < HP; ++h) x[h] = seen ? x[h] : -INFINITY;
+                for (int h = 0; h < HW; ++h) x[h] = seen ? x[h] : -INFINITY;
               }
               bool o0 = false, o1 = false, o2 = false, o3 = false;   // four chains of comparisons
 #pragma unroll
-              for (int h = 0; h < HP; h += 4) {
-                const float4 t = *reinterpret_cast<const float4*>(m->over + h);
+              for (int h = 0; h < HW; h += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(m->over + hb + h);
                 o0 |= x[h] > t.x;
                 o1 |= x[h + 1] > t.y;
                 o2 |= x[h + 2] > t.z;
@@ -919,20 +935,20 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             }
             ++gtile_s;
             // one vote: bit 0 of the barrier's OR says that some wait failed or some score is over
-            const bool any = named_bar_any(1, 128, failed || over);
+            const bool any = named_bar_any(1, SOFT, failed || over);
             if (any) {
-              if (named_bar_any(1, 128, failed)) {
+              if (named_bar_any(1, SOFT, failed)) {
                 failed = true;
                 break;
               }
-              float c[HP];
+              float c[HW];
 #pragma unroll
-              for (int h = 0; h < HP; ++h) c[h] = x[h];
-              warp_reduce_scatter<HP, true>(c, lane);
-              store_scattered<HP>(m->red[sw], c, lane);
-              named_bar_sync(1, 128);
-              if (t128 < HP) {
-                const int h = t128;
+              for (int h = 0; h < HW; ++h) c[h] = x[h];
+              warp_reduce_scatter<HW, true>(c, lane);
+              store_scattered<HW>(m->red[sw] + hb, c, lane);
+              named_bar_sync(1, SOFT);
+              if (ts < HP) {
+                const int h = ts;
                 const float top = fmaxf(fmaxf(m->red[0][h], m->red[1][h]), fmaxf(m->red[2][h], m->red[3][h]));
                 const float old = m->m_raw[h];
                 float al = 1.f;
@@ -944,15 +960,15 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
                 }
                 m->alpha[h] = al;
               }
-              named_bar_sync(1, 128);
+              named_bar_sync(1, SOFT);
 #pragma unroll
               for (int i = 0; i < HL; ++i) l[i] *= m->alpha[h_lane + i];
             }
             // weights; their fp32 sums per half page and head
-            uint32_t pw[HP / 2];
+            uint32_t pw[HW / 2];
 #pragma unroll
-            for (int h = 0; h < HP; h += 4) {
-              const float4 mm = *reinterpret_cast<const float4*>(m->m + h);
+            for (int h = 0; h < HW; h += 4) {
+              const float4 mm = *reinterpret_cast<const float4*>(m->m + hb + h);
               x[h] = ex2_approx(x[h] - mm.x);
               x[h + 1] = ex2_approx(x[h + 1] - mm.y);
               x[h + 2] = ex2_approx(x[h + 2] - mm.z);
@@ -962,17 +978,17 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             // each weight); the sums take the weights as they were before
             if (f16) {
 #pragma unroll
-              for (int h = 0; h < HP; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], true);
+              for (int h = 0; h < HW; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], true);
             } else {
 #pragma unroll
-              for (int h = 0; h < HP; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], false);
+              for (int h = 0; h < HW; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], false);
             }
-            warp_reduce_scatter<HP, false>(x, lane);
+            warp_reduce_scatter<HW, false>(x, lane);
 #pragma unroll
             for (int i = 0; i < HL; ++i) l[i] += x[i];
             if (a.score != nullptr && u < t1) {
               float2* uw = a.half_w + ((static_cast<long long>(r.b) * a.bt_stride + entry) * 2 + (sw & 1)) * a.H + h0;
-              if (HP >= 32 || (lane & 1) == 0) {
+              if (HW >= 32 || (lane & 1) == 0) {
 #pragma unroll
                 for (int i = 0; i < HL; ++i)
                   if (h_lane + i < G) uw[h_lane + i] = make_float2(x[i], m->m[h_lane + i]);
@@ -984,31 +1000,31 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             if (failed) continue;                // the next vote tells all warps
             tc_fence_after();
             if (any && j > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int db = 0; db < NDB; ++db) {
 #pragma unroll
-                for (int c = 0; c < HP / 16; ++c) {
-                  const uint32_t ta = tmem + lane_addr + 2 * HP + db * HP + 16 * c;
+                for (int c = 0; c < HW / 16; ++c) {
+                  const uint32_t ta = tmem + lane_addr + 2 * HP + db * HP + hb + 16 * c;
                   float o[16];
                   tmem_ld16(ta, o);
                   tmem_wait_ld();
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] *= m->alpha[16 * c + i];
+                  for (int i = 0; i < 16; ++i) o[i] *= m->alpha[hb + 16 * c + i];
                   tmem_st16(ta, o);
                 }
               }
               tmem_wait_st();
             }
 #pragma unroll
-            for (int c = 0; c < HP / 8; ++c)
-              *reinterpret_cast<uint4*>(sP + p_offset<HP>(row, c)) =
+            for (int c = 0; c < HW / 8; ++c)
+              *reinterpret_cast<uint4*>(sP + p_offset<HP>(row, hb / 8 + c)) =
                   make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->p_full);
             ++gtile_o;
-            if (dirty) {
+            if (dirty && hg == 0) {
               // Clear the rows that are not seen in each pair of V stages as it arrives. A wait on
               // a stage's phase is sound only when the phase before it is complete: the next
               // tile's K stages come before this V in the ring, so their product is awaited. Each
@@ -1037,7 +1053,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
               }
             }
           }
-          if (named_bar_any(1, 128, failed)) {
+          if (named_bar_any(1, SOFT, failed)) {
             failed = true;
             break;
           }
@@ -1045,11 +1061,11 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           // ------------------------------------------------------- segment epilogue
           failed = !__all_sync(0xffffffffu, mbar_wait(&m->pv_done, (gtile_o - 1) & 1, abort));
           tc_fence_after();
-          if (HP >= 32 || (lane & 1) == 0) {
+          if (HW >= 32 || (lane & 1) == 0) {
 #pragma unroll
             for (int i = 0; i < HL; ++i) m->red[sw][h_lane + i] = l[i];
           }
-          if (named_bar_any(1, 128, failed)) {
+          if (named_bar_any(1, SOFT, failed)) {
             failed = true;
             break;
           }
@@ -1058,44 +1074,44 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
           // workspace: the pages' weights are normalised by them.
           const bool whole = sg.u0 == 0 && sg.u1 == r.pages;
           const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(r.b) * a.Hkv + sg.kvh;
-          if (t128 == 127 && sg.u0 == 0) {
+          if (ts == 127 && sg.u0 == 0) {
             Pair pr;
             pr.slot = static_cast<int>(slot);
             pr.parts = whole ? 1 : m->split.holder(walk.seg_at + r.pages - 1) - static_cast<int>(blockIdx.x) + 1;
             a.pair[static_cast<long long>(r.b) * a.Hkv + sg.kvh] = pr;
           }
-          if (t128 < G) {
-            const float sum = m->red[0][t128] + m->red[1][t128] + m->red[2][t128] + m->red[3][t128];
-            a.part_ml[static_cast<long long>(t128) * a.slots + slot] = make_float2(m->m_raw[t128], sum);
-            m->alpha[t128] = sum == 0.f ? 0.f : 1.f / sum;
+          if (ts < G) {
+            const float sum = m->red[0][ts] + m->red[1][ts] + m->red[2][ts] + m->red[3][ts];
+            a.part_ml[static_cast<long long>(ts) * a.slots + slot] = make_float2(m->m_raw[ts], sum);
+            m->alpha[ts] = sum == 0.f ? 0.f : 1.f / sum;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1, SOFT);
           float* part = a.part_o + slot * G * a.d;
           SegWalk ahead = walk;
           Seg none;
           if (!whole && ri == nrec - 1 && !m->more && !ahead.next(r, none)) {
             // The CTA's last segment: the ring is idle, so each 128-dim block is laid out there
             // as it goes to memory, [head][128], and stored by one bulk copy.
-            const uint32_t base = smem_u32(sRing) + row * 4;
+            const uint32_t base = smem_u32(sRing) + hb * 512 + row * 4;
 #pragma unroll 1
             for (int db = 0; db < NDB; ++db) {
-              float o[HP];
-              tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
+              float o[HW];
+              tmem_ld_row<HW>(tmem + lane_addr + 2 * HP + db * HP + hb, o);
               tmem_wait_ld();
               const uint32_t to = base + db * G * 512;
               if (G == HP) {              // no branch between the common case's stores
 #pragma unroll
-                for (int h = 0; h < HP; ++h) st_shared_f32(to + h * 512, o[h]);
+                for (int h = 0; h < HW; ++h) st_shared_f32(to + h * 512, o[h]);
               } else {
 #pragma unroll
-                for (int h = 0; h < HP; ++h)
-                  if (h < G) st_shared_f32(to + h * 512, o[h]);
+                for (int h = 0; h < HW; ++h)
+                  if (hb + h < G) st_shared_f32(to + h * 512, o[h]);
               }
               fence_proxy_async_smem();
-              named_bar_sync(1, 128);
-              if (t128 == 0) bulk_store(part + db * G * 128, sRing + db * G * 512, G * 512);
+              named_bar_sync(1, SOFT);
+              if (ts == 0) bulk_store(part + db * G * 128, sRing + db * G * 512, G * 512);
             }
-            if (t128 == 0) {
+            if (ts == 0) {
               bulk_commit_and_wait();
               fence_proxy_async_global();
             }
@@ -1103,20 +1119,20 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             // Lanes hold one dim of every head. Quads exchange 4 x 4 so that a lane holds 4 dims
             // of one head: a store of a warp then covers 32 dims of 4 heads, whole 128-byte lines.
             const int quad = lane >> 2, i4 = lane & 3;
-            uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0 + i4) * a.d + sw * 32 + quad * 4;
-            float* po = part + i4 * 128 + sw * 32 + quad * 4;
+            uint16_t* fo = a.out + (static_cast<long long>(r.b) * a.H + h0 + hb + i4) * a.d + sw * 32 + quad * 4;
+            float* po = part + (hb + i4) * 128 + sw * 32 + quad * 4;
 #pragma unroll 1
             for (int db = 0; db < NDB; ++db, fo += 128, po += G * 128) {
-              float o[HP];
-              tmem_ld_row<HP>(tmem + lane_addr + 2 * HP + db * HP, o);
+              float o[HW];
+              tmem_ld_row<HW>(tmem + lane_addr + 2 * HP + db * HP + hb, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < HP; h += 4) {
-                if (h < G) {
+              for (int h = 0; h < HW; h += 4) {
+                if (hb + h < G) {
                   const float4 v = quad_transpose(o[h], o[h + 1], o[h + 2], o[h + 3], i4);
-                  if (h + i4 < G) {
+                  if (hb + h + i4 < G) {
                     if (whole) {
-                      const float inv = m->alpha[h + i4];
+                      const float inv = m->alpha[hb + h + i4];
                       *reinterpret_cast<uint2*>(fo + h * a.d) =
                           make_uint2(pack16(v.x * inv, v.y * inv, f16), pack16(v.z * inv, v.w * inv, f16));
                     } else {
@@ -1128,7 +1144,7 @@ __global__ void __launch_bounds__(NTHREADS, (Layout<HP, NDC>::CTAS_PER_SM))
             }
           }
           tc_fence_before();
-          named_bar_sync(1, 128);
+          named_bar_sync(1, SOFT);
         }
       }
     }
@@ -1440,7 +1456,7 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(lsa::paged::NTHREADS);
+  cfg.blockDim = dim3(lsa::paged::Roles<HP>::NT);
   cfg.dynamicSmemBytes = LY::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;

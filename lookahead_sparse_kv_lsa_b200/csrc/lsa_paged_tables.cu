@@ -68,19 +68,33 @@ __device__ __forceinline__ long long token_row(const AppendArgs& a, const Plan& 
   return (static_cast<long long>(page) * 2 * a.Hkv * PAGE + slot) * a.row16;
 }
 
-// Copy one token's K and V rows: 2 * Hkv * row16 pieces by `step` threads from `first`.
+// Copy one token's K and V rows: 2 * Hkv * row16 pieces by `step` threads from `first`, up to
+// eight loads of a thread in flight before its first store.
 __device__ __forceinline__ void copy_token(const AppendArgs& a, long long row, long long tok, int first, int step) {
   const int half = a.Hkv * a.row16;
   const uint4* ks = a.k_new + tok * half;
   const uint4* vs = a.v_new + tok * half;
   const long long head = static_cast<long long>(PAGE) * a.row16;    // pieces from head to head
   uint4* dst = a.pool + row;
-#pragma unroll 4
-  for (int i = first; i < half; i += step) {
-    const int h = i / a.row16, c = i - h * a.row16;
-    const uint4 k = ks[i], v = vs[i];
-    dst[h * head + c] = k;
-    dst[(a.Hkv + h) * head + c] = v;
+  for (int i0 = first; i0 < half; i0 += 4 * step) {
+    uint4 k[4], v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e * step;
+      if (i < half) {
+        k[e] = ks[i];
+        v[e] = vs[i];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e * step;
+      if (i < half) {
+        const int h = i / a.row16, c = i - h * a.row16;
+        dst[h * head + c] = k[e];
+        dst[(a.Hkv + h) * head + c] = v[e];
+      }
+    }
   }
 }
 
