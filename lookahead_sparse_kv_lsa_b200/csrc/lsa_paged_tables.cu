@@ -198,20 +198,71 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-struct EvictShared {
-  int cnt[2][32];
-  int cnt2[32];
+// The threads that trim one row: a block, or a cluster of CL blocks that exchange counts through
+// each other's shared memory. Words put before sync() are read by every warp of every block
+// after it.
+template <int CL, int NW>
+struct Team {
+  int words[13][CL * NW];   // 0 .. 3, 4 .. 7: sums in turn; 8 .. 10: smallest and largest key, numbers; 11: ties; 12: kept
 };
-
-// Sum of v over the block; one barrier, alternating buffers.
-__device__ __forceinline__ int block_sum(int v, EvictShared* s, int& which, int warp, int lane, int nwarps) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  if (nwarps == 1) return v;
-  if (lane == 0) s->cnt[which][warp] = v;
-  __syncthreads();
-  v = __reduce_add_sync(0xffffffffu, lane < nwarps ? s->cnt[which][lane] : 0);
+template <int CL>
+__device__ __forceinline__ int team_rank() {
+  if constexpr (CL == 1) return 0;
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+template <int CL>
+__device__ __forceinline__ void team_sync() {
+  if constexpr (CL == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+// Every lane of a warp calls; word `slot` of this warp is v in every block of the team.
+template <int CL, int NW>
+__device__ __forceinline__ void team_put(Team<CL, NW>* t, int set, int slot, int v, int lane) {
+  if constexpr (CL == 1) {
+    if (lane == 0) t->words[set][slot] = v;
+  } else if (lane < CL) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&t->words[set][slot])), "r"(lane));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+  }
+}
+// Sums of v[0 .. N) over the team; one barrier, alternating sets of words.
+template <int N, int CL, int NW>
+__device__ __forceinline__ void team_sum(int (&v)[N], Team<CL, NW>* t, int& which, int rank, int warp, int lane, int nwarps) {
+  static_assert(N <= 4, "words");
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __reduce_add_sync(0xffffffffu, v[k]);
+  if (CL == 1 && nwarps == 1) return;
+#pragma unroll
+  for (int k = 0; k < N; ++k) team_put(t, 4 * which + k, rank * nwarps + warp, v[k], lane);
+  team_sync<CL>();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 0;
+  for (int i = lane; i < CL * nwarps; i += 32) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += t->words[4 * which + k][i];
+  }
   which ^= 1;
-  return v;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __reduce_add_sync(0xffffffffu, v[k]);
+}
+template <int CL, int NW>
+__device__ __forceinline__ int team_sum(int v, Team<CL, NW>* t, int& which, int rank, int warp, int lane, int nwarps) {
+  int w[1] = {v};
+  team_sum(w, t, which, rank, warp, lane, nwarps);
+  return w[0];
+}
+// Sum of the words of the warps before this one in row order.
+template <int CL, int NW>
+__device__ __forceinline__ int team_before(const Team<CL, NW>* t, int set, int rank, int warp, int lane, int nwarps) {
+  int v = 0;
+  for (int i = lane; i < rank * nwarps + warp; i += 32) v += t->words[set][i];
+  return __reduce_add_sync(0xffffffffu, v);
 }
 
 // The counts of sequence b, checked, and written to dst. Returns false where nothing is to be
@@ -219,11 +270,12 @@ __device__ __forceinline__ int block_sum(int v, EvictShared* s, int& which, int 
 struct EvictRow {
   int n, have, gone;
 };
-__device__ __forceinline__ bool evict_begin(const EvictArgs& a, int b, int tid, int nt, EvictRow& r) {
+template <int CL>
+__device__ __forceinline__ bool evict_begin(const EvictArgs& a, int b, int rank, int tid, int nt, EvictRow& r) {
   r.n = a.src.n_entries[b];
   r.have = a.src.free_cnt[b];
   const int tail = a.src.tail_len[b];
-  __syncthreads();                          // the counts are read before any thread writes them
+  team_sync<CL>();                          // the counts are read before any thread writes them
   int bits = 0;
   if (r.n < 0 || r.n > a.bt_stride || r.have < 0 || r.have > a.free_stride) bits = LSA_DEVERR_BAD_SIZE;
   r.gone = bits == 0 && r.n > a.budget ? r.n - a.budget : 0;
@@ -231,7 +283,7 @@ __device__ __forceinline__ bool evict_begin(const EvictArgs& a, int b, int tid, 
     bits = LSA_DEVERR_POOL_CAPACITY;
     r.gone = 0;
   }
-  if (tid == 0) {
+  if (rank == 0 && tid == 0) {
     a.dst.n_entries[b] = r.n - r.gone;
     a.dst.free_cnt[b] = r.have + r.gone;
     a.dst.tail_len[b] = tail;
@@ -239,6 +291,7 @@ __device__ __forceinline__ bool evict_begin(const EvictArgs& a, int b, int tid, 
   }
   if (bits == LSA_DEVERR_BAD_SIZE) return false;
   if (r.gone > 0) return true;
+  if (rank != 0) return false;
   const long long row = static_cast<long long>(b) * a.bt_stride;
   if (a.dst.block_table != a.src.block_table)
     for (int i = tid; i < r.n; i += nt) a.dst.block_table[row + i] = a.src.block_table[row + i];
@@ -249,43 +302,51 @@ __device__ __forceinline__ bool evict_begin(const EvictArgs& a, int b, int tid, 
   return false;
 }
 
-// A CTA per sequence, the whole row's scores in registers (PER a thread, entry tid + i * nt; NaN
-// in place of what is not a middle entry, so that no comparison counts it).
+// A block (CL = 1) or a cluster of CL blocks per sequence, the whole row's scores in registers: PER
+// a thread, block `rank` holding the entries [rank * share, (rank + 1) * share), thread tid of it
+// every nt-th (NaN in place of what is not a middle entry, so that no comparison counts it).
 //
 // Threshold: the (budget - sink - recent)-th largest score, by its key T, bit by bit from the
-// first bit in which the keys differ; each bit is one comparison per score and one count over
-// the block, and the search ends early when a candidate keeps exactly as many as wanted, or
+// first bit in which the keys differ; a bit (a cluster: three) takes a comparison per score and
+// candidate and one exchange of counts, and the search ends early when a candidate keeps exactly as many as wanted, or
 // before it begins when the smallest score is the threshold (pages that were never attended).
-// Placement: per (chunk of nt entries, warp) counts of the kept entries, one scan of them, then
-// kept entries go to the front and freed pages onto the stack, four chunks at a time. Chunks
-// are read before any of them is written, and entries only move towards the front, so dst may
-// be src.
-// Bound by the latency of some 15 block-wide counts and of the three arrays, and, for rows of
-// thousands, by the instructions of the one SM that holds the row.
-template <int PER, int MAXT>
+// Placement: counts of the kept entries per (chunk of nt entries, warp), one scan of them, then
+// kept entries go to the front and freed pages onto the stack. The whole row is read before
+// any of it is written, so dst may be src.
+// Bound by the latency of the exchanges, some 15 in a block and 6 in a cluster, and of the three
+// arrays.
+template <int PER, int MAXT, int CL>
 __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ EvictArgs a) {
+  constexpr int NW = MAXT / 32;
+  // bits per exchange: a block counts faster than it compares (64 rows of up to 4,096: 470 cycles a
+  // bit, 2,030 for three), a cluster's barrier costs more (16,385 entries: 1,510, and 2,900)
+  constexpr int BITS = CL == 1 ? 1 : 3, CANDS = (1 << BITS) - 1;
   static_assert(PER <= 32, "a bit per entry, a thread per (chunk, warp)");
-  __shared__ EvictShared sh;
-  __shared__ int place[PER * (MAXT / 32)];
+  static_assert(PER * MAXT * CL < 65536, "counts of 16 bits");
+  __shared__ Team<CL, NW> team;
+  __shared__ int place[PER * NW], place_warp[NW];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = team_rank<CL>();
+  const int b = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = blockDim.x, nwarps = nt >> 5;
   const long long row = static_cast<long long>(b) * a.bt_stride;
   EvictRow r;
-  if (!evict_begin(a, b, tid, nt, r)) return;
+  if (!evict_begin<CL>(a, b, rank, tid, nt, r)) return;
+  const int n = r.n, m0 = a.n_sink, m1 = n - a.n_recent;   // the middle entries: [m0, m1)
+  const int want = a.budget - a.n_sink - a.n_recent;       // of them are kept: 0 <= want < m1 - m0
+  const int share = (n + CL - 1) / CL;                     // <= PER * nt
+  const int e0 = rank * share + tid, e_end = min(n, (rank + 1) * share);
   const int32_t* table = a.src.block_table + row;
   const int32_t* bpos = a.src.block_pos ? a.src.block_pos + row : nullptr;
   const float* score = a.src.score + row;
-  const int n = r.n, m0 = a.n_sink, m1 = n - a.n_recent;   // the middle entries: [m0, m1)
-  const int want = a.budget - a.n_sink - a.n_recent;       // of them are kept: 0 <= want < m1 - m0
   const float none = __int_as_float(0x7fffffff);
   float s[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = tid + i * nt;
+    const int e = e0 + i * nt;
     s[i] = none;
-    if (i * nt < m1 && e >= m0 && e < m1) s[i] = score[e];
+    if (e >= m0 && e < m1 && e < e_end) s[i] = score[e];
   }
   int which = 0;
   // How a score is judged: kept where it is above f (or also where equal, if `geq`); of the
@@ -305,17 +366,23 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
     uint32_t klo = __reduce_min_sync(0xffffffffu, score_key(lo));
     uint32_t khi = __reduce_max_sync(0xffffffffu, score_key(hi));
     real = __reduce_add_sync(0xffffffffu, real);
-    if (nwarps > 1) {
-      if (lane == 0) {
-        sh.cnt[0][warp] = static_cast<int>(klo);
-        sh.cnt[1][warp] = static_cast<int>(khi);
-        sh.cnt2[warp] = real;
+    if (CL > 1 || nwarps > 1) {
+      const int own = rank * nwarps + warp;
+      team_put(&team, 8, own, static_cast<int>(klo), lane);
+      team_put(&team, 9, own, static_cast<int>(khi), lane);
+      team_put(&team, 10, own, real, lane);
+      team_sync<CL>();
+      klo = 0xffffffffu;
+      khi = 0u;
+      real = 0;
+      for (int i = lane; i < CL * nwarps; i += 32) {
+        klo = min(klo, static_cast<uint32_t>(team.words[8][i]));
+        khi = max(khi, static_cast<uint32_t>(team.words[9][i]));
+        real += team.words[10][i];
       }
-      __syncthreads();
-      klo = __reduce_min_sync(0xffffffffu, lane < nwarps ? static_cast<uint32_t>(sh.cnt[0][lane]) : 0xffffffffu);
-      khi = __reduce_max_sync(0xffffffffu, lane < nwarps ? static_cast<uint32_t>(sh.cnt[1][lane]) : 0u);
-      real = __reduce_add_sync(0xffffffffu, lane < nwarps ? sh.cnt2[lane] : 0);
-      __syncthreads();
+      klo = __reduce_min_sync(0xffffffffu, klo);
+      khi = __reduce_max_sync(0xffffffffu, khi);
+      real = __reduce_add_sync(0xffffffffu, real);
     }
     if (real <= want) {                                    // all numbers stay, and the first NaNs
       f = -INFINITY;
@@ -327,7 +394,7 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
       int above = 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) above += s[i] > f;
-      above = block_sum(above, &sh, which, warp, lane, nwarps);
+      above = team_sum(above, &team, which, rank, warp, lane, nwarps);
       ties = want - above;                                 // > 0: the smallest score is the threshold
       if (above == want) {
         ties = 0;
@@ -335,17 +402,30 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
         int bit = 31 - __clz(klo ^ khi);                   // all keys share the bits above
         uint32_t T = bit == 31 ? 0u : klo & ~((2u << bit) - 1u);
         int c = real;
-        for (; bit >= 0 && c != want; --bit) {
-          const uint32_t cand = T | (1u << bit);
-          f = key_score(cand);
-          int k = 0;
+        while (bit >= 0 && c != want) {
+          // BITS bits at a time: how many scores reach each of the candidates
+          const int bits = min(BITS, bit + 1), shift = bit + 1 - bits;
+          float g[CANDS + 1];
 #pragma unroll
-          for (int i = 0; i < PER; ++i) k += s[i] >= f;
-          k = block_sum(k, &sh, which, warp, lane, nwarps);
-          if (k >= want) {
-            T = cand;
-            c = k;
+          for (int j = 1; j <= CANDS; ++j)
+            g[j] = j < (1 << bits) ? key_score(T | (static_cast<uint32_t>(j) << shift)) : none;
+          int k[(CANDS + 1) / 2] = {};                     // two counts a word: both stay below 2^16
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+#pragma unroll
+            for (int j = 1; j <= CANDS; ++j) k[(j - 1) / 2] += s[i] >= g[j] ? (j & 1 ? 1 : 1 << 16) : 0;
           }
+          team_sum(k, &team, which, rank, warp, lane, nwarps);
+#pragma unroll
+          for (int j = CANDS; j >= 1; --j) {
+            const int reach = j & 1 ? k[(j - 1) / 2] & 0xffff : static_cast<int>(static_cast<uint32_t>(k[(j - 1) / 2]) >> 16);
+            if (reach >= want) {                           // the largest candidate that enough scores reach
+              T |= static_cast<uint32_t>(j) << shift;
+              c = reach;
+              break;
+            }
+          }
+          bit -= bits;
         }
         f = key_score(T);
         if (c == want) {
@@ -355,27 +435,52 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
           above = 0;
 #pragma unroll
           for (int i = 0; i < PER; ++i) above += s[i] > f;
-          ties = want - block_sum(above, &sh, which, warp, lane, nwarps);
+          ties = want - team_sum(above, &team, which, rank, warp, lane, nwarps);
         }
       }
     }
   }
-  // which entries stay: bit i for entry tid + i * nt
-  uint32_t keep = 0;
-  int tied = 0;
+  // pages, positions and scores of the row, all read before any is written
+  int page[PER], pos[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (i * nt >= n) continue;
-    const int e = tid + i * nt;
+    if (CL == 1 && i * nt >= n) break;
+    const int e = e0 + i * nt;
+    page[i] = e < e_end ? table[e] : 0;
+    pos[i] = e < e_end && bpos ? bpos[e] : 0;
+    if (e < e_end && (e < m0 || e >= m1)) s[i] = score[e];
+  }
+  // the ties before this block, where some but not all of them stay
+  int tied = 0;
+  if (ties > 0) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = e0 + i * nt;
+      mine += e >= m0 && e < m1 && e < e_end && (nan_ties ? s[i] != s[i] : s[i] == f);
+    }
+    if (CL > 1) {
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      team_put(&team, 11, rank * nwarps + warp, mine, lane);
+      team_sync<CL>();
+      tied = team_before(&team, 11, rank, 0, lane, nwarps);
+    }
+  }
+  // which entries stay: bit i for entry e0 + i * nt
+  uint32_t keep = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (CL == 1 && i * nt >= n) break;
+    const int e = e0 + i * nt;
     const bool mid = e >= m0 && e < m1;
-    bool stay = s[i] > f || (geq && s[i] == f) || (e < n && !mid);
-    if (tied < ties) {                                     // (uniform: there are ties left to place)
-      const bool tie = mid && (nan_ties ? s[i] != s[i] : s[i] == f);
+    bool stay = e < e_end && (!mid || s[i] > f || (geq && s[i] == f));
+    if (tied < ties) {                                     // (uniform in the block: some ties are left to place)
+      const bool tie = e < e_end && mid && (nan_ties ? s[i] != s[i] : s[i] == f);
       const unsigned mask = __ballot_sync(0xffffffffu, tie);
       __syncthreads();
-      if (lane == 0) sh.cnt2[warp] = __popc(mask);
+      if (lane == 0) place_warp[warp] = __popc(mask);
       __syncthreads();
-      const int tw = lane < nwarps ? sh.cnt2[lane] : 0;
+      const int tw = lane < nwarps ? place_warp[lane] : 0;
       const int before = __reduce_add_sync(0xffffffffu, lane < warp ? tw : 0);
       if (tie && tied + before + __popc(mask & ((1u << lane) - 1u)) < ties) stay = true;
       tied += __reduce_add_sync(0xffffffffu, tw);
@@ -385,8 +490,8 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
     if (lane == 0) place[i * nwarps + warp] = __popc(mask);
   }
   __syncthreads();
-  // exclusive scan of the counts, a thread each
-  const int cells = (n + nt - 1) / nt * nwarps;
+  // exclusive scan of the counts, a thread each; then the kept entries of the blocks before
+  const int cells = (CL == 1 ? min(PER, (n + nt - 1) / nt) : PER) * nwarps;
   const int v = tid < cells ? place[tid] : 0;
   int incl = v;
 #pragma unroll
@@ -394,45 +499,34 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
     const int t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
-  if (lane == 31) sh.cnt2[warp] = incl;
-  __syncthreads();
-  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.cnt2[lane] : 0);
+  if (CL > 1) team_put(&team, 12, rank * nwarps + warp, __shfl_sync(0xffffffffu, incl, 31), lane);
+  if (CL == 1 && lane == 31) place_warp[warp] = incl;
+  team_sync<CL>();
+  int before;
+  if constexpr (CL > 1)
+    before = team_before(&team, 12, rank, warp, lane, nwarps);
+  else
+    before = __reduce_add_sync(0xffffffffu, lane < warp ? place_warp[lane] : 0);
   if (tid < cells) place[tid] = before + incl - v;
   __syncthreads();
   int32_t* o_table = a.dst.block_table + row;
   int32_t* o_pos = a.dst.block_pos ? a.dst.block_pos + row : nullptr;
   float* o_score = a.dst.score + row;
   int32_t* push = a.dst.free_list + static_cast<long long>(b) * a.free_stride + r.have;
-  constexpr int STEP = 4;
-  static_assert(PER % STEP == 0, "chunks");
-  int page[STEP], pos[STEP];
-  float sc[STEP];
 #pragma unroll
-  for (int i0 = 0; i0 < PER; i0 += STEP) {
-    if (i0 * nt >= n) break;
-#pragma unroll
-    for (int i = 0; i < STEP; ++i) {
-      const int e = tid + (i0 + i) * nt;
-      const bool stay = (keep >> (i0 + i)) & 1u;           // positions and scores go with kept entries only
-      page[i] = e < n ? table[e] : 0;
-      pos[i] = stay && bpos ? bpos[e] : 0;
-      sc[i] = stay ? score[e] : 0.f;
-    }
-    __syncthreads();                     // these chunks are read
-#pragma unroll
-    for (int i = 0; i < STEP; ++i) {
-      const int e = tid + (i0 + i) * nt;
-      const bool stay = (keep >> (i0 + i)) & 1u;
-      const unsigned mask = __ballot_sync(0xffffffffu, stay);
-      if (e < n) {
-        const int to = place[(i0 + i) * nwarps + warp] + __popc(mask & ((1u << lane) - 1u));
-        if (stay) {
-          o_table[to] = page[i];
-          if (o_pos) o_pos[to] = pos[i];
-          o_score[to] = sc[i];
-        } else {
-          push[e - to] = page[i];        // entries freed before this one
-        }
+  for (int i = 0; i < PER; ++i) {
+    if (CL == 1 && i * nt >= n) break;
+    const int e = e0 + i * nt;
+    const bool stay = (keep >> i) & 1u;
+    const unsigned mask = __ballot_sync(0xffffffffu, stay);
+    if (e < e_end) {
+      const int to = place[i * nwarps + warp] + __popc(mask & ((1u << lane) - 1u));
+      if (stay) {
+        o_table[to] = page[i];
+        if (o_pos) o_pos[to] = pos[i];
+        o_score[to] = s[i];
+      } else {
+        push[e - to] = page[i];        // entries freed before this one
       }
     }
   }
@@ -441,14 +535,14 @@ __global__ void __launch_bounds__(MAXT) evict_kernel(const __grid_constant__ Evi
 // Rows longer than the registers hold: the same search over keys read again for each bit, and
 // the placement a chunk of nt entries at a time.
 __global__ void __launch_bounds__(1024) evict_long_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ EvictShared sh;
+  __shared__ Team<1, 32> team;
   grid_dependency_wait();
   grid_dependents_launch();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = blockDim.x, nwarps = nt >> 5;
   const long long row = static_cast<long long>(b) * a.bt_stride;
   EvictRow r;
-  if (!evict_begin(a, b, tid, nt, r)) return;
+  if (!evict_begin<1>(a, b, 0, tid, nt, r)) return;
   const int32_t* table = a.src.block_table + row;
   const int32_t* bpos = a.src.block_pos ? a.src.block_pos + row : nullptr;
   const float* score = a.src.score + row;
@@ -465,12 +559,12 @@ __global__ void __launch_bounds__(1024) evict_long_kernel(const __grid_constant_
       const uint32_t cand = T | (1u << bit);
       int c = 0;
       for (int e = m0 + tid; e < m1; e += nt) c += score_key(score[e]) >= cand;
-      c = block_sum(c, &sh, which, warp, lane, nwarps);
+      c = team_sum(c, &team, which, 0, warp, lane, nwarps);
       if (c >= want) T = cand;
     }
     int above = 0;
     for (int e = m0 + tid; e < m1; e += nt) above += score_key(score[e]) > T;
-    ties = want - block_sum(above, &sh, which, warp, lane, nwarps);
+    ties = want - team_sum(above, &team, which, 0, warp, lane, nwarps);
   }
   int32_t* push = a.dst.free_list + static_cast<long long>(b) * a.free_stride + r.have;
   int kept = 0, tied = 0;                                // so far, in earlier chunks
@@ -485,17 +579,17 @@ __global__ void __launch_bounds__(1024) evict_long_kernel(const __grid_constant_
     const bool tie = mid && want > 0 && k == T;
     const unsigned below = (1u << lane) - 1u;
     const unsigned tmask = __ballot_sync(0xffffffffu, tie);
-    __syncthreads();                                     // cnt is free, and the last chunk is written
-    if (lane == 0) sh.cnt[0][warp] = __popc(tmask);
+    __syncthreads();                                     // the words are free, and the last chunk is written
+    if (lane == 0) team.words[11][warp] = __popc(tmask);
     __syncthreads();
-    const int tw = lane < nwarps ? sh.cnt[0][lane] : 0;
+    const int tw = lane < nwarps ? team.words[11][lane] : 0;
     const int t_before = __reduce_add_sync(0xffffffffu, lane < warp ? tw : 0);
     const int t_all = __reduce_add_sync(0xffffffffu, tw);
     const bool keep = live && (!mid || (want > 0 && (k > T || (tie && tied + t_before + __popc(tmask & below) < ties))));
     const unsigned kmask = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) sh.cnt2[warp] = __popc(kmask);
+    if (lane == 0) team.words[12][warp] = __popc(kmask);
     __syncthreads();                                     // also: every entry of the chunk is read
-    const int kw = lane < nwarps ? sh.cnt2[lane] : 0;
+    const int kw = lane < nwarps ? team.words[12][lane] : 0;
     const int k_before = __reduce_add_sync(0xffffffffu, lane < warp ? kw : 0);
     const int to = kept + k_before + __popc(kmask & below);
     if (keep) {
@@ -520,21 +614,30 @@ using lsa::paged_tables::AppendArgs;
 using lsa::paged_tables::EvictArgs;
 
 template <typename... Args>
-lsa_status launch(void (*kern)(Args...), unsigned grid, unsigned block, void* stream, const Args&... args) {
-  cudaLaunchAttribute attr[1];
+lsa_status launch_clusters(void (*kern)(Args...), unsigned teams, unsigned cluster, unsigned block, void* stream,
+                           const Args&... args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(teams * cluster);
   cfg.blockDim = dim3(block);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
     cudaGetLastError();
     return LSA_ERR_CUDA;
   }
   return LSA_OK;
+}
+
+template <typename... Args>
+lsa_status launch(void (*kern)(Args...), unsigned grid, unsigned block, void* stream, const Args&... args) {
+  return launch_clusters(kern, grid, 1, block, stream, args...);
 }
 
 // dst's arrays: all that the call writes must be there; block_pos and score exactly where
@@ -609,15 +712,16 @@ extern "C" lsa_status lsa_paged_evict(const lsa_paged_cache* c, int32_t budget, 
   a.n_sink = n_sink;
   a.n_recent = n_recent;
   // Up to 8 scores a thread: a warp alone needs no barriers for rows of up to 256 entries (65
-  // entries: 1 warp X us, 3 warps Y us), then blocks of up to 512. Longer rows take 24 a thread,
-  // and rows that do not fit the registers of a block are read again for each bit.
+  // entries: 2.9 us), then blocks of up to 512 threads (64 rows of up to 4,096: 9.9 us), then clusters
+  // of 8 such blocks; rows longer than that are read again for each bit.
   const int stride = c->bt_stride;
   const unsigned B = static_cast<unsigned>(c->B);
   if (stride <= 8 * 512) {
     const unsigned threads = stride <= 256 ? 32 : (stride + 255) / 256 * 32;
-    return launch(lsa::paged_tables::evict_kernel<8, 512>, B, threads, stream, a);
+    return launch(lsa::paged_tables::evict_kernel<8, 512, 1>, B, threads, stream, a);
   }
-  if (stride <= 24 * 768)
-    return launch(lsa::paged_tables::evict_kernel<24, 768>, B, static_cast<unsigned>((stride + 767) / 768 * 32), stream, a);
+  if (stride <= 8 * 8 * 512)
+    return launch_clusters(lsa::paged_tables::evict_kernel<8, 512, 8>, B, 8,
+                           static_cast<unsigned>((stride + 8 * 256 - 1) / (8 * 256) * 32), stream, a);
   return launch(lsa::paged_tables::evict_long_kernel, B, 1024, stream, a);
 }

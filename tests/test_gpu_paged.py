@@ -525,7 +525,8 @@ def check_evict(n, budget, sink, recent, score=None, in_place=True, pos=True, se
     ([1], 1, 0, 1), ([2], 1, 0, 1), ([5, 0, 3, 4], 3, 1, 1), ([65] * 8, 64, 1, 16), ([65, 64, 63, 200], 64, 30, 34),
     ([1000, 3, 999, 512], 100, 0, 1), ([4097, 4096, 1], 512, 4, 64), ([16385], 1351, 1, 129), ([20000, 17000], 5000, 2, 3),
     ([33] * 70, 20, 5, 5), ([256, 255, 250], 250, 3, 3), ([257, 300], 100, 0, 2), ([4096, 100], 99, 1, 1), ([4097], 4096, 1, 1),
-    ([18432, 18431], 18431, 1, 1), ([18433, 5], 9000, 100, 100)], ids=str)
+    ([18432, 18431], 18431, 1, 1), ([4097, 5, 0, 4100, 33], 20, 4, 9), ([32768, 40, 7], 9000, 100, 100),
+    ([32769, 5], 9000, 100, 100)], ids=str)
 def test_evict(cuda_ok, n, budget, sink, recent, in_place):
     check_evict(n, budget, sink, recent, in_place=in_place, seed=len(n), pos=budget != 100)
 
@@ -555,8 +556,8 @@ def test_evict_ties_and_odd_scores(cuda_ok, kind):
     check_evict(n, 13, 3, 10, score=s, seed=5, in_place=False)
     wide = np.tile(s, (1, 4))                      # rows of more scores a thread
     check_evict([5900, 4200, 64, 6000], 2001, 3, 10, score=wide, seed=6)
-    long = np.tile(s, (1, 13))                     # rows that are read again
-    check_evict([19000, 300, 64, 19500], 2001, 3, 10, score=long, seed=7)
+    long = np.tile(s, (1, 22))                     # rows that are read again
+    check_evict([33000, 300, 64, 32900], 2001, 3, 10, score=long, seed=7)
 
 
 def test_evict_full_stack_and_bad_sizes(cuda_ok):
@@ -566,7 +567,7 @@ def test_evict_full_stack_and_bad_sizes(cuda_ok):
 
 
 def test_evict_long_rows(cuda_ok):
-    """Rows whose keys do not fit the registers of a block."""
+    """Rows whose keys do not fit the registers of a cluster."""
     check_evict([50000, 40], 3001, 7, 9, seed=8)
 
 
