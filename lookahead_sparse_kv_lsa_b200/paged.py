@@ -66,6 +66,8 @@ class LsaPagedTables:
             _check(tail_len, i32, "tail_len", (B,), dev),
             _check(free_list, i32, "free_list", (B, self.free_stride), dev),
             _check(free_cnt, i32, "free_cnt", (B,), dev))
+        self.ref = C.byref(self.c)
+        self.layout = (B, E, self.free_stride, dev)
 
     @classmethod
     def allocate(cls, B: int, entries: int, pages_per_seq: int, device, score: bool = True,
@@ -153,10 +155,9 @@ class LsaPagedCache:
     def _dst(self, dst: Optional[LsaPagedTables]):
         if dst is None:
             return None
-        t = self.tables
-        if (dst.B, dst.bt_stride, dst.free_stride, dst.device) != (t.B, t.bt_stride, t.free_stride, t.device):
+        if dst.layout != self.tables.layout:
             raise ValueError("dst must have the shapes and the device of the cache's tables")
-        return C.byref(dst.c)
+        return dst.ref
 
     def attend(self, q, out, stream=None) -> None:
         """One new token of every sequence over the cache (lsa_paged_attn). q, out: [B][H][d];
@@ -167,11 +168,13 @@ class LsaPagedCache:
     def append(self, k, v, tok_off=None, dst: Optional[LsaPagedTables] = None, stream=None) -> None:
         """New tokens behind every sequence's last (lsa_paged_append). k, v: [tokens][Hkv][d];
         tok_off: i32 [B+1], or None for one token per sequence."""
-        n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else self.B
+        n = self.B if tok_off is None else k.shape[0]
         shape = (n, self.Hkv, self.d)
+        off = None
+        if tok_off is not None:
+            off = _check(tok_off, torch.int32, "tok_off", (self.B + 1,), self.device)
         self._call("lsa_paged_append", stream, _check(k, self.dtype, "k", shape, self.device),
-                   _check(v, self.dtype, "v", shape, self.device), n,
-                   _check(tok_off, torch.int32, "tok_off", (self.B + 1,), self.device), self._dst(dst))
+                   _check(v, self.dtype, "v", shape, self.device), n, off, self._dst(dst))
 
     def evict(self, budget: int, n_sink: int = 1, n_recent: int = 1,
               dst: Optional[LsaPagedTables] = None, stream=None) -> None:
