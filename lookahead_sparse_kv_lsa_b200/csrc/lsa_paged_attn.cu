@@ -163,6 +163,12 @@ __device__ __forceinline__ void warm_up(const Args& a, int tid) {
   if (tid == 5 && a.slopes) prefetch_l2(a.slopes);
 }
 
+// Slots of block `block` that lie below position x.
+__device__ __forceinline__ int slots_below(long long block, long long x) {
+  const long long k = x - block * PAGE;
+  return k <= 0 ? 0 : k >= PAGE ? PAGE : static_cast<int>(k);
+}
+
 // Everything that depends on one sequence. The four per-sequence words are loaded together,
 // then (only where a mask or a bias needs them) the positions of the row's ends.
 __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
@@ -200,9 +206,9 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
       const bool hole = r.e1 > r.e2;                          // one entry holds both bounds
       if (hole) r.e1 = r.e2;
       // slots before the window in its first entry, slots of the prefix in its last
-      const int k_low = r.e2 < n ? static_cast<int>(max(0ll, low - (pos ? pos[r.e2] : r.e2) * static_cast<long long>(PAGE))) : 0;
-      const int k_pre = r.e1 > 0 ? static_cast<int>(min(static_cast<long long>(PAGE), r.pre - (pos ? pos[r.e1 - 1] : r.e1 - 1) *
-                                                                                          static_cast<long long>(PAGE))) : PAGE;
+      int k_low = 0, k_pre = PAGE;
+      if (r.e2 < n) k_low = slots_below(pos ? pos[r.e2] : r.e2, low);
+      if (r.e1 > 0) k_pre = slots_below(pos ? pos[r.e1 - 1] : r.e1 - 1, r.pre);
       r.shift_pre = k_pre - PAGE;
       if (hole) {
         r.dirty = r.e1;
@@ -1185,6 +1191,14 @@ struct JoinArgs {
 };
 
 constexpr int JOIN_WARPS = JOIN_THREADS / 32;
+// The parts of a pair. After a call whose waits ran out (LSA_DEVERR_TIMEOUT) a pair may hold
+// anything; what would lead outside the workspace reads as no parts.
+__device__ __forceinline__ Pair load_pair(const Args& a, int b, int kvh) {
+  Pair p = a.pair[static_cast<long long>(b) * a.Hkv + kvh];
+  if (p.slot < 0 || p.parts < 0 || p.parts > MAX_CTAS || p.slot > a.slots - p.parts) p.slot = p.parts = 0;
+  return p;
+}
+
 // A part that saw nothing has weight 0 (its max is -inf), and its values are dropped whatever
 // they are.
 __device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
@@ -1231,7 +1245,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
   grid_dependents_launch();
   if (outs) {
     if (ob >= a.B) return;
-    const Pair pr = a.pair[static_cast<long long>(ob) * a.Hkv + okv];
+    const Pair pr = load_pair(a, ob, okv);
     const int n = pr.parts;
     if (n == 1) return;                         // written by the CTA that held the pair whole
     uint16_t* out = a.out + static_cast<long long>(item) * a.d + chunk * 128 + lane * 4;
@@ -1342,7 +1356,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int h = min(h0 + e, a.H - 1), kvh = h / G;
-        const Pair pr = a.pair[static_cast<long long>(b) * a.Hkv + kvh];
+        const Pair pr = load_pair(a, b, kvh);
         ml[e] = a.part_ml + static_cast<long long>(h - kvh * G) * a.slots + pr.slot;
         n[e] = pr.parts;
         most = max(most, n[e]);

@@ -168,7 +168,7 @@ class LsaPagedCache:
     def append(self, k, v, tok_off=None, dst: Optional[LsaPagedTables] = None, stream=None) -> None:
         """New tokens behind every sequence's last (lsa_paged_append). k, v: [tokens][Hkv][d];
         tok_off: i32 [B+1], or None for one token per sequence."""
-        n = self.B if tok_off is None else k.shape[0]
+        n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else self.B
         shape = (n, self.Hkv, self.d)
         off = None
         if tok_off is not None:

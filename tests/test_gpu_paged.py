@@ -331,6 +331,22 @@ def test_workspace_carries_no_state(cuda_ok):
     assert torch.equal(c.out, first)
 
 
+def test_positions_out_of_order_stay_in_bounds(cuda_ok):
+    """What such a table attends to is not specified; nothing outside it is read, and its neighbours
+    are right."""
+    rng = np.random.default_rng(0)
+    for kw in (dict(window=300), dict(prefix=[500] * 4, docs=[900] * 4), dict(slopes=[0.1] * 8, window=700, prefix=[70] * 4)):
+        c = Case([1500, 900, 1200, 640], 8, 2, 128, seed=15, junk=False, **kw)
+        pos = c.pos.copy()
+        pos[0] = rng.permutation(c.E)
+        pos[1] = rng.integers(-5, 1 << 25, c.E)
+        pos[3] = 7
+        c.tables.block_pos.copy_(i32(pos))
+        c.run()
+        assert c.cache.read_err() == 0
+        c.check(seqs=[2])
+
+
 def test_far_offsets(cuda_ok):
     # a pool past 2^32 bytes: pages near its end
     H, d = 8, 128
