@@ -1184,9 +1184,10 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
 
 // ------------------------------------------------------------------------ joining
 struct JoinArgs {
-  int out_blocks;    // blocks that join outputs; the rest add the pages' weights
+  int score_blocks;  // blocks that add the pages' weights, the first ones because they take longest;
+                     //   the rest join outputs
   int wide;          // a block per (sequence, head, 128 dims); else a warp
-  int entries;       // table entries per block of the second kind
+  int entries;       // table entries per block of the first kind
   int chunks;        //   and such blocks per sequence
 };
 
@@ -1236,9 +1237,10 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
   if (tid == 1) prefetch_l2(a.part_o);
   if (tid == 2) prefetch_l2(a.out);
   if (tid == 3 && a.score) prefetch_l2(a.score);
-  const bool outs = static_cast<int>(blockIdx.x) < ja.out_blocks;
+  const int out_block = static_cast<int>(blockIdx.x) - ja.score_blocks;
+  const bool outs = out_block >= 0;
   const int chunks = a.d / 128;
-  const int job = ja.wide ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
+  const int job = ja.wide ? out_block : out_block * JOIN_WARPS + warp;
   const int item = job / chunks, chunk = job - item * chunks;
   const int ob = item / a.H, oh = item - ob * a.H, okv = oh / G;
   grid_dependency_wait();
@@ -1299,14 +1301,14 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
     for (int e = 0; e < 8; ++e)
       if (warp + e * JOIN_WARPS < n) v[e] = *reinterpret_cast<const float4*>(part + (warp + e * JOIN_WARPS) * stride);
     float top = -INFINITY;
-#pragma unroll 5
+#pragma unroll 1
     for (int k = lane; k < n; k += 32) top = fmaxf(top, ml[k].x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // each warp keeps the weights of its own parts, k = warp mod 8
     float* w = sm;
     float sum = 0.f;
-#pragma unroll 5
+#pragma unroll 1
     for (int k = lane; k < n; k += 32) {
       const float2 x = ml[k];
       const float wk = part_weight(x.x, top);
@@ -1337,7 +1339,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
     return;
   }
   // -------- the pages' weights
-  const int blk = blockIdx.x - ja.out_blocks;
+  const int blk = blockIdx.x;
   const int b = blk / ja.chunks, j0 = (blk - b * ja.chunks) * ja.entries;
   const Plan p = a.plan[b];
   if (j0 >= p.n) return;
@@ -1361,6 +1363,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
         n[e] = pr.parts;
         most = max(most, n[e]);
       }
+#pragma unroll 1
       for (int k = lane; k < most; k += 64) {
         float2 v[8];
 #pragma unroll
@@ -1488,8 +1491,7 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   // a block for each 128 dims of a head where pairs are split over 24 CTAs or more on average
   ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
   const int warps = lsa::paged::JOIN_WARPS;
-  ja.out_blocks = static_cast<int>(ja.wide ? items : (items + warps - 1) / warps);
-  long long blocks = ja.out_blocks;
+  long long blocks = ja.wide ? items : (items + warps - 1) / warps;
   if (a.score != nullptr) {
     // two blocks per SM over the tables, at least four entries each
     const long long total = static_cast<long long>(a.B) * a.bt_stride;
@@ -1497,7 +1499,8 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
     per = (per + 3) / 4 * 4;
     ja.entries = static_cast<int>(per);
     ja.chunks = static_cast<int>((a.bt_stride + per - 1) / per);
-    blocks += static_cast<long long>(a.B) * ja.chunks;
+    ja.score_blocks = a.B * ja.chunks;
+    blocks += ja.score_blocks;
   }
   const size_t sm_wide = lsa::paged::MAX_CTAS * sizeof(float) + lsa::paged::JOIN_THREADS * sizeof(float4);
   const size_t sm_score = a.score ? static_cast<size_t>(a.H) * sizeof(float2) : 0;
