@@ -10,7 +10,12 @@
 //
 // What bounds it: every key and value is read once, 4 d Hkv bytes a token against
 // 4 H d flops, so H / Hkv flop per byte; on a B200 that is HBM bandwidth for any group of
-// up to 64 heads, as long as the products run on the tensor cores.
+// up to 64 heads, as long as the products run on the tensor cores. Measured (profiler: the DRAM
+// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512, 354 us for 2.15 GB, 93 % of
+// the copy bandwidth; a ragged batch of 64 with 8 key heads of 128, 57.9 us for 261 MB, 69 %; some
+// 1,350 kept pages of the 1M tokens, 52.5 us for 177 MB, 51 %. Below some 500 MB the fixed
+// costs count: planning and the first tile (about 4 us), the last product and the epilogue
+// (3 to 4 us), the joining kernel (1 us to start, 3 to 8 us), and segments that end unevenly.
 //
 // Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
 // e2 on (document, window), the same for each key head. Every pair (sequence, key head) with
@@ -485,8 +490,14 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
   __syncthreads();
 }
 
-// Fixed cost of a segment in pages, and the least share of pages that a CTA is started for.
-__host__ __device__ constexpr int overhead_pages(int) { return 5; }
+// Fixed cost of a segment in pages. A least-squares fit over the CTAs of a ragged batch of 8 heads
+// of 128 gives 1.5 us a segment and 1.9 us a tile of two pages beside 8 us that every CTA pays, and
+// 64 heads of 512 give 4.0, 3.8 and 10 us; charging more than that pays, because it also keeps
+// short segments, whose tiles are not full, apart. 64 ragged sequences / 8 of 128K tokens took
+// 66.6 / 61.7 us with 2 / 3 pages, 58.3 / 57.5 us with 4 / 5, 59.2 / 57.7 us with 6.
+constexpr int OVERHEAD_PAGES = 5;
+// The least share of pages that a CTA is started for: 256 pages of 8 heads of 128 took 14.6 us in
+// shares of 1, 12.6 us of 2, 13.0 us of 4.
 __host__ __device__ constexpr int least_pages(int d) { return d >= 256 ? 1 : 2; }
 
 // Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
@@ -540,18 +551,15 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
   return d;
 }
 
-// x = c tanh(k x) for a row of scores, c in log2 units: tanh t = 1 - 2 / (1 + 2^(2 t log2 e)) is
-// off by a few 2^-24 in absolute terms, so a capped score by c times that. Up to SMALL_CAP that
-// is no more than the rounding of a score near the cap; above it small scores would lose, and
-// where |t| < 1/16 the Taylor series t (1 - t^2/3 + 2 t^4/15) is used (relative error below
-// 17/315 t^6 < 4e-9). The special functions of 16 heads are issued together, so that their
-// latencies overlap.
-constexpr float SMALL_CAP = 64.0f * LOG2E;
-template <int HP, bool SERIES>
-__device__ __forceinline__ void cap_scores(float (&x)[HP], float k, float c) {
+// x = c tanh(k x) for a row of scores, c in log2 units. tanh t = 1 - 2 / (1 + 2^(2 t log2 e)) is off
+// by a few 2^-24 in absolute terms; where |t| < 1/16 that is much of the result, and the Taylor
+// series t (1 - t^2/3 + 2 t^4/15) is used (relative error below 17/315 t^6 < 4e-9). The special
+// functions of 16 heads are issued together, so that their latencies overlap.
+template <int HW>
+__device__ __forceinline__ void cap_scores(float (&x)[HW], float k, float c) {
   const float k2 = 2.f * LOG2E * k;
 #pragma unroll
-  for (int h = 0; h < HP; h += 16) {
+  for (int h = 0; h < HW; h += 16) {
     float e[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(x[h + i] * k2));
@@ -559,14 +567,9 @@ __device__ __forceinline__ void cap_scores(float (&x)[HP], float k, float c) {
     for (int i = 0; i < 16; ++i) asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(1.f + e[i]));
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float big = fmaf(-2.f * c, e[i], c);
-      if constexpr (SERIES) {
-        const float t = x[h + i] * k, t2 = t * t;
-        const float small = c * t * fmaf(t2, fmaf(t2, 2.f / 15.f, -1.f / 3.f), 1.f);
-        x[h + i] = fabsf(t) < 0.0625f ? small : big;
-      } else {
-        x[h + i] = big;
-      }
+      const float t = x[h + i] * k, t2 = t * t;
+      const float small = c * t * fmaf(t2, fmaf(t2, 2.f / 15.f, -1.f / 3.f), 1.f);
+      x[h + i] = fabsf(t) < 0.0625f ? small : fmaf(-2.f * c, e[i], c);
     }
   }
 }
@@ -905,10 +908,7 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
               __syncwarp();
               if (lane == 0) mbar_arrive(&m->s_free[sb]);
               if (a.cap > 0.f) {
-                if (cap2 <= SMALL_CAP)
-                  cap_scores<HW, false>(x, scale2, cap2);
-                else
-                  cap_scores<HW, true>(x, scale2, cap2);
+                cap_scores<HW>(x, scale2, cap2);
               } else {
 #pragma unroll
                 for (int h = 0; h < HW; ++h) x[h] *= scale2;
@@ -1467,7 +1467,7 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   auto kern = lsa::paged::paged_attn_kernel<HP, NDC>;
   const lsa_status st = lsa_host::ensure_smem_limit(reinterpret_cast<const void*>(kern), LY::SMEM);
   if (st != LSA_OK) return st;
-  a.overhead = lsa::paged::overhead_pages(NDC * 64);
+  a.overhead = lsa::paged::OVERHEAD_PAGES;
   a.min_pages = lsa::paged::least_pages(NDC * 64);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1488,7 +1488,9 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   }
   JoinArgs ja = {};
   const long long items = static_cast<long long>(a.B) * a.H * (a.d / 128);
-  // a block for each 128 dims of a head where pairs are split over 24 CTAs or more on average
+  // A block for each 128 dims of a head where pairs are split over 24 CTAs or more on average, else
+  // a warp: one sequence of 16K or 1M tokens takes 12.7 or 52.5 us with blocks, 18.9 or 69.9 us with
+  // warps; 8 of 128K or 64 ragged ones take 58.8 or 61.9 us with blocks, 55.9 or 57.7 us with warps.
   ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
   const int warps = lsa::paged::JOIN_WARPS;
   long long blocks = ja.wide ? items : (items + warps - 1) / warps;
@@ -1573,6 +1575,8 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   CUtensorMap mkv, mq;
   st = lsa_host::encode_tiled_planes(&mkv, c->pool, c->d, LSA_BLOCK, static_cast<uint64_t>(c->n_pages) * 2 * c->Hkv);
   if (st != LSA_OK) return st;
+  // Heads padded to the next size: a ragged batch of 8 heads a group takes 57.9 us in the kernel for
+  // 16, 69 us in the one for 32, 92 us in the one for 64.
   const int HP = G <= 16 ? 16 : G <= 32 ? 32 : 64;
   st = lsa_host::encode_tiled_rows(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H, HP);
   if (st != LSA_OK) return st;

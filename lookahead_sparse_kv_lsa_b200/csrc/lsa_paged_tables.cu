@@ -711,13 +711,14 @@ extern "C" lsa_status lsa_paged_evict(const lsa_paged_cache* c, int32_t budget, 
   a.budget = budget;
   a.n_sink = n_sink;
   a.n_recent = n_recent;
-  // Up to 8 scores a thread: a warp alone needs no barriers for rows of up to 256 entries (65
-  // entries: 2.9 us), then blocks of up to 512 threads (64 rows of up to 4,096: 9.9 us), then clusters
-  // of 8 such blocks; rows longer than that are read again for each bit.
+  // A block of up to 512 threads, 8 scores each at most (65 entries: 2.7 us with 3 warps, 3.3 us with
+  // one; 64 rows of up to 4,096: 9.9 us, 16.4 us in clusters), then clusters of 8 such blocks
+  // (16,385 entries: 15.6 us; read again for each bit by one block, 79 us), and rows longer
+  // than a cluster's registers hold are read again.
   const int stride = c->bt_stride;
   const unsigned B = static_cast<unsigned>(c->B);
   if (stride <= 8 * 512) {
-    const unsigned threads = stride <= 256 ? 32 : (stride + 255) / 256 * 32;
+    const unsigned threads = stride <= 512 ? (stride + 31) / 32 * 32 : 512;
     return launch(lsa::paged_tables::evict_kernel<8, 512, 1>, B, threads, stream, a);
   }
   if (stride <= 8 * 8 * 512)
