@@ -1187,6 +1187,7 @@ struct JoinArgs {
   int score_blocks;  // blocks that add the pages' weights, the first ones because they take longest;
                      //   the rest join outputs
   int wide;          // a block per (sequence, head, 128 dims); else a warp
+  int few;           // most pairs have few parts: their weights' normalisers take a thread per head
   int entries;       // table entries per block of the first kind
   int chunks;        //   and such blocks per sequence
 };
@@ -1344,8 +1345,32 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
   const Plan p = a.plan[b];
   if (j0 >= p.n) return;
   float2* fin = reinterpret_cast<float2*>(sm);                 // [H]: (M, 1 / L)
-  if (p.pages > 0) {
-    // a warp takes four heads at a time, a lane every 32nd part
+  // (M, 1 / L) of every head. Pairs of few parts: a thread per head
+  constexpr int FEW = 8;
+  bool many = !ja.few && p.pages > 0;
+  if (ja.few && p.pages > 0) {
+    for (int h = tid; h < a.H; h += JOIN_THREADS) {
+      const int kvh = h / G;
+      const Pair pr = load_pair(a, b, kvh);
+      const float2* ml = a.part_ml + static_cast<long long>(h - kvh * G) * a.slots + pr.slot;
+      many |= pr.parts > FEW;
+      float2 v[FEW];
+      float t = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < FEW; ++k) {
+        v[k] = k < pr.parts ? ml[k] : make_float2(-INFINITY, 0.f);
+        t = fmaxf(t, v[k].x);
+      }
+#pragma unroll
+      for (int k = 0; k < FEW; ++k) {
+        const float w = part_weight(v[k].x, t);
+        if (w != 0.f) l = fmaf(w, v[k].y, l);
+      }
+      fin[h] = make_float2(t, l == 0.f ? 0.f : 1.f / l);
+    }
+  }
+  if (__syncthreads_or(many)) {
+    // pairs of many parts: a warp takes four heads at a time, a lane every 32nd part
     for (int h0 = 4 * warp; h0 < a.H; h0 += 4 * JOIN_WARPS) {
       float M[4], L[4];
 #pragma unroll
@@ -1492,6 +1517,10 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   // a warp: one sequence of 16K or 1M tokens takes 12.7 or 52.5 us with blocks, 18.9 or 69.9 us with
   // warps; 8 of 128K or 64 ragged ones take 58.8 or 61.9 us with blocks, 55.9 or 57.7 us with warps.
   ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
+  // Where a pair is split over two CTAs or fewer on average, a thread forms a head's normaliser (64
+  // ragged sequences: 53.2 us, 57.4 us with a warp per four heads); else a warp does (8 of 128K: 56.1
+  // us, 58.6 us with the threads tried first).
+  ja.few = static_cast<long long>(a.B) * a.Hkv * 2 >= ctas;
   const int warps = lsa::paged::JOIN_WARPS;
   long long blocks = ja.wide ? items : (items + warps - 1) / warps;
   if (a.score != nullptr) {
