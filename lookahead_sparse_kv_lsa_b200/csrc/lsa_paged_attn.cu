@@ -1187,7 +1187,7 @@ struct JoinArgs {
   int score_blocks;  // blocks that add the pages' weights, the first ones because they take longest;
                      //   the rest join outputs
   int wide;          // a block per (sequence, head, 128 dims); else a warp
-  int few;           // most pairs have few parts: their weights' normalisers take a thread per head
+  int per_head;      // threads that form a head's normaliser: a power of two, 1 .. 32
   int entries;       // table entries per block of the first kind
   int chunks;        //   and such blocks per sequence
 };
@@ -1345,81 +1345,45 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4)
   const Plan p = a.plan[b];
   if (j0 >= p.n) return;
   float2* fin = reinterpret_cast<float2*>(sm);                 // [H]: (M, 1 / L)
-  // (M, 1 / L) of every head. Pairs of few parts: a thread per head
-  constexpr int FEW = 8;
-  bool many = !ja.few && p.pages > 0;
-  if (ja.few && p.pages > 0) {
-    for (int h = tid; h < a.H; h += JOIN_THREADS) {
-      const int kvh = h / G;
+  // (M, 1 / L) of every head, by `per_head` neighbouring threads that take every per_head-th part,
+  // eight on their way at a time
+  if (p.pages > 0) {
+    const int sub = tid & (ja.per_head - 1), step = JOIN_THREADS / ja.per_head;
+    for (int h0 = 0; h0 < a.H; h0 += step) {
+      const int at = h0 + tid / ja.per_head, h = min(at, a.H - 1), kvh = h / G;
       const Pair pr = load_pair(a, b, kvh);
       const float2* ml = a.part_ml + static_cast<long long>(h - kvh * G) * a.slots + pr.slot;
-      many |= pr.parts > FEW;
-      float2 v[FEW];
-      float t = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int k = 0; k < FEW; ++k) {
-        v[k] = k < pr.parts ? ml[k] : make_float2(-INFINITY, 0.f);
-        t = fmaxf(t, v[k].x);
-      }
-#pragma unroll
-      for (int k = 0; k < FEW; ++k) {
-        const float w = part_weight(v[k].x, t);
-        if (w != 0.f) l = fmaf(w, v[k].y, l);
-      }
-      fin[h] = make_float2(t, l == 0.f ? 0.f : 1.f / l);
-    }
-  }
-  if (__syncthreads_or(many)) {
-    // pairs of many parts: a warp takes four heads at a time, a lane every 32nd part
-    for (int h0 = 4 * warp; h0 < a.H; h0 += 4 * JOIN_WARPS) {
-      float M[4], L[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        M[e] = -INFINITY;
-        L[e] = 0.f;
-      }
-      const float2* ml[4];
-      int n[4], most = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int h = min(h0 + e, a.H - 1), kvh = h / G;
-        const Pair pr = load_pair(a, b, kvh);
-        ml[e] = a.part_ml + static_cast<long long>(h - kvh * G) * a.slots + pr.slot;
-        n[e] = pr.parts;
-        most = max(most, n[e]);
-      }
+      float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-      for (int k = lane; k < most; k += 64) {
+      for (int k = sub; k < pr.parts; k += 8 * ja.per_head) {
         float2 v[8];
+        float t = M;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int i = k + 32 * (e & 1);
-          v[e] = i < n[e / 2] ? ml[e / 2][i] : make_float2(-INFINITY, 0.f);
+          const int i = k + e * ja.per_head;
+          v[e] = i < pr.parts ? ml[i] : make_float2(-INFINITY, 0.f);
+          t = fmaxf(t, v[e].x);
         }
+        L *= part_weight(M, t);
+        M = t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float t = fmaxf(M[e], fmaxf(v[2 * e].x, v[2 * e + 1].x));
-          L[e] *= part_weight(M[e], t);
-          M[e] = t;
-          const float w0 = part_weight(v[2 * e].x, t), w1 = part_weight(v[2 * e + 1].x, t);
-          if (w0 != 0.f) L[e] = fmaf(w0, v[2 * e].y, L[e]);
-          if (w1 != 0.f) L[e] = fmaf(w1, v[2 * e + 1].y, L[e]);
+        for (int e = 0; e < 8; ++e) {
+          const float w = part_weight(v[e].x, M);
+          if (w != 0.f) L = fmaf(w, v[e].y, L);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float t = M[e];
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-        const float w = part_weight(M[e], t);
-        float l = w == 0.f ? 0.f : L[e] * w;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0 && h0 + e < a.H) fin[h0 + e] = make_float2(t, l == 0.f ? 0.f : 1.f / l);
+      __syncwarp();
+      for (int o = ja.per_head >> 1; o >= 1; o >>= 1) {
+        const float M2 = __shfl_xor_sync(0xffffffffu, M, o), L2 = __shfl_xor_sync(0xffffffffu, L, o);
+        const float t = fmaxf(M, M2);
+        const float w = part_weight(M, t), w2 = part_weight(M2, t);
+        L = (w == 0.f ? 0.f : L * w) + (w2 == 0.f ? 0.f : L2 * w2);
+        M = t;
       }
+      if (sub == 0 && at < a.H) fin[at] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
     }
-    __syncthreads();
   }
+  __syncthreads();
   // a warp takes four entries at a time, so that their loads overlap
   const int j1 = min(p.n, j0 + ja.entries);
   for (int j = j0 + 4 * warp; j < j1; j += 4 * JOIN_WARPS) {
@@ -1517,10 +1481,8 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   // a warp: one sequence of 16K or 1M tokens takes 12.7 or 52.5 us with blocks, 18.9 or 69.9 us with
   // warps; 8 of 128K or 64 ragged ones take 58.8 or 61.9 us with blocks, 55.9 or 57.7 us with warps.
   ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
-  // Where a pair is split over two CTAs or fewer on average, a thread forms a head's normaliser (64
-  // ragged sequences: 53.2 us, 57.4 us with a warp per four heads); else a warp does (8 of 128K: 56.1
-  // us, 58.6 us with the threads tried first).
-  ja.few = static_cast<long long>(a.B) * a.Hkv * 2 >= ctas;
+  ja.per_head = 1;
+  while (ja.per_head < 32 && 2 * ja.per_head * a.H <= lsa::paged::JOIN_THREADS) ja.per_head *= 2;
   const int warps = lsa::paged::JOIN_WARPS;
   long long blocks = ja.wide ? items : (items + warps - 1) / warps;
   if (a.score != nullptr) {
