@@ -11,11 +11,11 @@
 // What bounds it: every key and value is read once, 4 d Hkv bytes a token against
 // 4 H d flops, so H / Hkv flop per byte; on a B200 that is HBM bandwidth for any group of
 // up to 64 heads, as long as the products run on the tensor cores. Measured (profiler: the DRAM
-// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512, 354 us for 2.15 GB, 93 % of
-// the copy bandwidth; a ragged batch of 64 with 8 key heads of 128, 57.9 us for 261 MB, 69 %; some
-// 1,350 kept pages of the 1M tokens, 52.5 us for 177 MB, 51 %. Below some 500 MB the fixed
-// costs count: planning and the first tile (about 4 us), the last product and the epilogue
-// (3 to 4 us), the joining kernel (1 us to start, 3 to 8 us), and segments that end unevenly.
+// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512, 354 to 359 us for 2.15 GB,
+// 91 to 93 % of the copy bandwidth; a ragged batch of 64 with 8 key heads of 128, 52.5 us for 261
+// MB, 76 %; some 1,350 kept pages of the 1M tokens, 48.9 us for 177 MB, 55 %. Below some 500 MB the
+// fixed costs count: planning and the first tile (about 4 us), the last product and the epilogue
+// (3 to 4 us), the joining kernel (1 us to start, 3 to 5 us), and segments that end unevenly.
 //
 // Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
 // e2 on (document, window), the same for each key head. Every pair (sequence, key head) with
@@ -493,12 +493,12 @@ __device__ __forceinline__ void plan_cta(const Args& a, int B, bool dry, int ski
 
 // Fixed cost of a segment in pages. A least-squares fit over the CTAs of a ragged batch of 8 heads
 // of 128 gives 1.5 us a segment and 1.9 us a tile of two pages beside 8 us that every CTA pays, and
-// 64 heads of 512 give 4.0, 3.8 and 10 us; charging more than that pays, because it also keeps
-// short segments, whose tiles are not full, apart. 64 ragged sequences / 8 of 128K tokens took
-// 66.6 / 61.7 us with 2 / 3 pages, 58.3 / 57.5 us with 4 / 5, 59.2 / 57.7 us with 6.
+// 64 heads of 512 give 4.0, 3.8 and 10 us; but a segment of one page, whose latencies nothing
+// hides, costs as much as five. 64 ragged sequences / 8 of 128K tokens take 60.8 / 57.5 us with 2
+// pages, 54.8 / 53.4 us with 3, 52.5 / 52.9 us with 5, 54.3 / 52.4 us with 7.
 constexpr int OVERHEAD_PAGES = 5;
-// The least share of pages that a CTA is started for: 256 pages of 8 heads of 128 took 14.6 us in
-// shares of 1, 12.6 us of 2, 13.0 us of 4.
+// The least share of pages that a CTA is started for: 256 pages of 8 heads of 128 take 14.5 us in
+// shares of 1, 11.7 us of 2, 12.5 us of 4.
 __host__ __device__ constexpr int least_pages(int d) { return d >= 256 ? 1 : 2; }
 
 // Shared-memory layout. The ring's stage pairs hold two adjacent 64-dim halves of V, so the
@@ -1482,8 +1482,8 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   JoinArgs ja = {};
   const long long items = static_cast<long long>(a.B) * a.H * (a.d / 128);
   // A block for each 128 dims of a head where pairs are split over 24 CTAs or more on average, else
-  // a warp: one sequence of 16K or 1M tokens takes 12.7 or 52.5 us with blocks, 18.9 or 69.9 us with
-  // warps; 8 of 128K or 64 ragged ones take 58.8 or 61.9 us with blocks, 55.9 or 57.7 us with warps.
+  // a warp: one sequence of 16K or 1M tokens takes 11.7 or 48.9 us with blocks, 19.1 or 64.9 us with
+  // warps; 8 of 128K or 64 ragged ones take 60.5 or 63.1 us with blocks, 52.9 or 52.5 us with warps.
   ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
   ja.per_head = 1;
   while (ja.per_head < 32 && 2 * ja.per_head * a.H <= lsa::paged::JOIN_THREADS) ja.per_head *= 2;
@@ -1572,8 +1572,8 @@ extern "C" lsa_status lsa_paged_attn(const lsa_paged_cache* c, const uint16_t* q
   CUtensorMap mkv, mq;
   st = lsa_host::encode_tiled_planes(&mkv, c->pool, c->d, LSA_BLOCK, static_cast<uint64_t>(c->n_pages) * 2 * c->Hkv);
   if (st != LSA_OK) return st;
-  // Heads padded to the next size: a ragged batch of 8 heads a group takes 57.9 us in the kernel for
-  // 16, 69 us in the one for 32, 92 us in the one for 64.
+  // Heads padded to the next size: a ragged batch of 8 heads a group takes 52.5 us in the kernel for
+  // 16, 66 us in the one for 32, 94 us in the one for 64.
   const int HP = G <= 16 ? 16 : G <= 32 ? 32 : 64;
   st = lsa_host::encode_tiled_rows(&mq, q, c->d, static_cast<uint64_t>(c->B) * c->H, HP);
   if (st != LSA_OK) return st;
