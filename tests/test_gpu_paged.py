@@ -657,6 +657,68 @@ def test_a_bounded_cache_decodes(cuda_ok):
         assert sorted(held + free) == list(range(b * 14, (b + 1) * 14))
 
 
+def test_two_caches_on_two_streams(cuda_ok):
+    """Caches of their own, at the same time: each gets what it gets alone."""
+    cs = [Case([30000, 41, 700], 16, 4, 128, seed=8, cap=30.0), Case([9000, 400], 64, 1, 512, "fp16", seed=9)]
+    alone = [c.run().out.clone() for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    qs = [c.q.to(DEV) for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, st in zip(cs, qs, streams):
+            c.out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for c, q, st in zip(cs, qs, streams):
+                c.cache.attend(q, c.out, stream=st)
+        torch.cuda.synchronize()
+        for c, o in zip(cs, alone):
+            assert torch.equal(c.out, o) and c.cache.read_err() == 0
+
+
+def test_a_captured_step_decodes(cuda_ok):
+    """append, attend and evict of one step in a graph: replays advance the cache as calls do."""
+    B, H, Hkv, d, budget = 5, 16, 4, 128, 5
+    g = torch.Generator().manual_seed(1)
+    prompt = [300, 0, 1, 64, 447]
+    off = i32(np.concatenate([[0], np.cumsum(prompt)]))
+    kp, vp = (torch.randn((sum(prompt), Hkv, d), generator=g).to(torch.float16).to(DEV) for _ in range(2))
+    steps = [[torch.randn(s, generator=g).to(torch.float16).to(DEV) for s in ((B, Hkv, d), (B, Hkv, d), (B, H, d))]
+             for _ in range(140)]
+    got = []
+    for captured in (False, True):
+        t = lsa.LsaPagedTables.allocate(B, 10, 12, DEV)
+        pool = torch.full((B * 12, 2, Hkv, 64, d), float("nan"), dtype=torch.float16, device=DEV)
+        c = lsa.LsaPagedCache(pool, t, H, cap=20.0, window=200, prefix_len=i32([10, 0, 64, 1, 70]), decay=0.9)
+        c.append(kp, vp, off)
+        k, v, q = (x.clone() for x in steps[0])
+        out = torch.empty((B, H, d), dtype=torch.float16, device=DEV)
+
+        def step():
+            c.append(k, v)
+            c.attend(q, out)
+            c.evict(budget, 1, 2)
+
+        graph = None
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        outs = []
+        for s in steps:
+            for x, y in zip((k, v, q), s):
+                x.copy_(y)
+            graph.replay() if captured else step()
+            outs.append(out.clone())
+        torch.cuda.synchronize()
+        assert c.read_err() == 0
+        got.append((torch.stack(outs), t))
+    assert torch.equal(got[0][0], got[1][0])
+    for name in ("block_table", "block_pos", "score", "n_entries", "tail_len", "free_list", "free_cnt"):
+        assert torch.equal(getattr(got[0][1], name), getattr(got[1][1], name)), name
+    assert torch.isfinite(got[0][0].float()).all()
+
+
 def test_binding_refusals(cuda_ok):
     c = Case([100, 10], 8, 2, 128, seed=1)
     q = c.q.to(DEV)
