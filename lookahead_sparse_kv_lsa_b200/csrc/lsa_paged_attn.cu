@@ -11,8 +11,9 @@
 // What bounds it: every key and value is read once, 4 d Hkv bytes a token against
 // 4 H d flops, so H / Hkv flop per byte; on a B200 that is HBM bandwidth for any group of
 // up to 64 heads, as long as the products run on the tensor cores. Measured (profiler: the DRAM
-// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512, 354 to 359 us for 2.15 GB,
-// 91 to 93 % of the copy bandwidth; a ragged batch of 64 with 8 key heads of 128, 52.5 us for 261
+// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512, 352 us for 2.15 GB, 93 % of
+// the copy bandwidth, or 365 to 390 us where the power cap holds the SMs at 1.6 to 1.7 GHz (a tile
+// takes a CTA some 10,400 cycles); a ragged batch of 64 with 8 key heads of 128, 52.5 us for 261
 // MB, 76 %; some 1,350 kept pages of the 1M tokens, 48.9 us for 177 MB, 55 %. Below some 500 MB the
 // fixed costs count: planning and the first tile (about 4 us), the last product and the epilogue
 // (3 to 4 us), the joining kernel (1 us to start, 3 to 5 us), and segments that end unevenly.
