@@ -21,10 +21,10 @@
 // Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
 // e2 on (document, window), the same for each key head. Every pair (sequence, key head) with
 // anything to see costs its pages plus a fixed overhead (filling and draining the pipeline),
-// and the costs of all pairs, in order, are divided evenly over the CTAs; each (CTA, pair) piece is a segment that leaves (O, max, sum) in the
-// workspace slot CTA + pair, and the joining kernel, a programmatic dependent launch, merges the slots of
-// a pair. Nothing waits for another CTA and no counter outlives a call, so a workspace
-// carries no state.
+// and the costs of all pairs, in order, are divided evenly over the CTAs; each (CTA, pair)
+// piece is a segment that leaves (O, max, sum) in the workspace slot CTA + pair, and the
+// joining kernel, a programmatic dependent launch, merges the slots of a pair. Nothing waits
+// for another CTA and no counter outlives a call, so a workspace carries no state.
 //
 // Within a segment, tiles of two pages run newest first (a bias that falls with the
 // distance then sets the running max once), in a pipeline of three roles:
