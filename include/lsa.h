@@ -491,7 +491,10 @@ lsa_status lsa_paged_check(const lsa_paged_cache* c);
  *   out[b][h] = sum_x w_h(x) V(x)
  *   score[b][j] = decay * score[b][j] + sum_h sum_(x in entry j) w_h(x),  j < n_entries[b]
  *
- * A sequence that sees nothing (n_entries 0, or all its positions masked) gets zeros.
+ * A sequence that sees nothing (n_entries 0, or all its positions masked) gets zeros, and so
+ * does a head whose scores are all -inf. A NaN in q or in a key that is seen makes the head's
+ * output NaN, and the score of every page with a seen position; a NaN in a value that is seen
+ * makes its dimension of the output NaN, also where its weight is 0 in fp32.
  * Positions that are not seen have no influence whatever their keys and values hold,
  * infinities and NaN included, and blocks without a seen position are not read. The new
  * token's own key and value must be in the cache (lsa_paged_append).

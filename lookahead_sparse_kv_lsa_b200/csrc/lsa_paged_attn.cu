@@ -120,7 +120,7 @@ struct Args {
   Pair* pair;        // [B][Hkv]
   float2* part_ml;   // [G][slots] running max (log2 units) and sum
   float* part_o;     // [slot][d/128][G][128]
-  float2* half_w;    // [B][bt_stride][2][H] half pages' sums and the max they refer to
+  float2* half_w;    // [B][bt_stride][2][H] half pages' sums and the max they refer to (-inf: unseen)
   long long n_pages;
   int B, H, Hkv, G, d, bt_stride, window, f16;
   int slots;         // of the workspace's parts
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
             }
             const int entry = u < t1 ? page_entry(r, u) : 0;
             const bool seen = u < t1 && page >= 0 && page < a.n_pages && slot_seen(r, entry, in_page, x0);
-            const bool all_seen = __all_sync(0xffffffffu, seen);
+            const unsigned sees = __ballot_sync(0xffffffffu, seen);   // of this half page
             const int sb = gtile_s & 1;
             if (!failed)
               failed = !__all_sync(0xffffffffu, mbar_wait(&m->s_full[sb], (gtile_s >> 1) & 1, abort));
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
                   x[h + 3] = fmaf(s.w, rel, x[h + 3]);
                 }
               }
-              if (!all_seen) {
+              if (sees != 0xffffffffu) {
 #pragma unroll
                 for (int h = 0; h < HW; ++h) x[h] = seen ? x[h] : -INFINITY;
               }
@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
               if (HW >= 32 || (lane & 1) == 0) {
 #pragma unroll
                 for (int i = 0; i < HL; ++i)
-                  if (h_lane + i < G) uw[h_lane + i] = make_float2(x[i], m->m[h_lane + i]);
+                  if (h_lane + i < G) uw[h_lane + i] = make_float2(x[i], sees ? m->m[h_lane + i] : -INFINITY);
               }
             }
             // the previous tile's product must be done before P is overwritten or O rescaled
@@ -1090,7 +1090,9 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
           }
           if (ts < G) {
             const float sum = m->red[0][ts] + m->red[1][ts] + m->red[2][ts] + m->red[3][ts];
-            a.part_ml[static_cast<long long>(ts) * a.slots + slot] = make_float2(m->m_raw[ts], sum);
+            // a sum that is NaN (a score is, or infinite) stands in for the max too: comparisons pass
+            // over NaN, so the max may be -inf, or so low that the part would get no weight
+            a.part_ml[static_cast<long long>(ts) * a.slots + slot] = make_float2(sum == sum ? m->m_raw[ts] : sum, sum);
             m->alpha[ts] = sum == 0.f ? 0.f : 1.f / sum;
           }
           named_bar_sync(1, SOFT);
@@ -1203,17 +1205,16 @@ __device__ __forceinline__ Pair load_pair(const Args& a, int b, int kvh) {
   return p;
 }
 
-// A part that saw nothing has weight 0 (its max is -inf), and its values are dropped whatever
-// they are.
+// A part that saw nothing has the max -inf, weight 0, and zeros as sum and values. Every part is
+// added, whatever its weight: NaN in its values, or as its max, reaches the output as it does where
+// one CTA holds the pair whole.
 __device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
 
 __device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) {
-  if (w != 0.f) {
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
+  acc.x = fmaf(w, v.x, acc.x);
+  acc.y = fmaf(w, v.y, acc.y);
+  acc.z = fmaf(w, v.z, acc.z);
+  acc.w = fmaf(w, v.w, acc.w);
 }
 
 __device__ __forceinline__ void store_out(uint16_t* p, float4 v, float inv, bool f16) {
@@ -1275,7 +1276,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 3)
         const float old = part_weight(top, t);
         top = t;
         const float w = part_weight(mine.x, top);
-        float s = w == 0.f ? 0.f : w * mine.y;
+        float s = w * mine.y;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         sum = sum * old + s;
@@ -1319,7 +1320,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 3)
     for (int e = 0; e < LANE_PARTS; ++e) {
       const float wk = part_weight(x[e].x, top);
       if (lane + 32 * e < n && (lane & (JOIN_WARPS - 1)) == warp) w[lane + 32 * e] = wk;
-      sum += wk == 0.f ? 0.f : wk * x[e].y;
+      sum = fmaf(wk, x[e].y, sum);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -1372,20 +1373,16 @@ __global__ void __launch_bounds__(JOIN_THREADS, 3)
         L *= part_weight(M, t);
         M = t;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float w = part_weight(v[e].x, M);
-          if (w != 0.f) L = fmaf(w, v[e].y, L);
-        }
+        for (int e = 0; e < 8; ++e) L = fmaf(part_weight(v[e].x, M), v[e].y, L);
       }
       __syncwarp();
       for (int o = ja.per_head >> 1; o >= 1; o >>= 1) {
         const float M2 = __shfl_xor_sync(0xffffffffu, M, o), L2 = __shfl_xor_sync(0xffffffffu, L, o);
         const float t = fmaxf(M, M2);
-        const float w = part_weight(M, t), w2 = part_weight(M2, t);
-        L = (w == 0.f ? 0.f : L * w) + (w2 == 0.f ? 0.f : L2 * w2);
+        L = L * part_weight(M, t) + L2 * part_weight(M2, t);
         M = t;
       }
-      if (sub == 0 && at < a.H) fin[at] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+      if (sub == 0 && at < a.H) fin[at] = make_float2(M == -INFINITY ? 0.f : M, L == 0.f ? 0.f : 1.f / L);
     }
   }
   __syncthreads();
@@ -1403,11 +1400,13 @@ __global__ void __launch_bounds__(JOIN_THREADS, 3)
       for (int h = lane; h < a.H; h += 32) {
         float2 w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = live[e / 2] ? hw[e * a.H + h] : make_float2(0.f, 0.f);
+        for (int e = 0; e < 8; ++e) w[e] = live[e / 2] ? hw[e * a.H + h] : make_float2(0.f, -INFINITY);
         const float2 f = fin[h];
+        // (a sum of 0 may refer to a max that was not set yet; where the head's normaliser is NaN,
+        // every half page that is seen gets it)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (w[e].x != 0.f) mass[e / 2] += w[e].x * ex2_approx(w[e].y - f.x) * f.y;
+          if (w[e].y != -INFINITY) mass[e / 2] += (w[e].x == 0.f ? 0.f : w[e].x * ex2_approx(w[e].y - f.x)) * f.y;
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) {
