@@ -63,6 +63,10 @@ constexpr int STAGE_BYTES = TILE * 128;   // [128 rows][64 dims] 16-bit = 16 KB
 constexpr int MAXREC = 32;                // sequences a CTA plans at a time
 constexpr int YRING = 128;                // pages that the producer has looked up
 constexpr float RESCALE_LOG2 = 8.0f;      // raise the running max only by more than 2^8
+// fp16 weights are 2^7 times as large (the reference that scores are taken relative to lies 7
+// below the running max): fp16 is subnormal below 2^-14 and 0 below 2^-25, and the small weights of a
+// long row add up. They are at most 2^(7 + 8), half of what fp16 holds.
+constexpr float LIFT_F16_LOG2 = 7.0f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int JOIN_THREADS = 256;
 constexpr int MAX_CTAS = 320;
@@ -118,7 +122,7 @@ struct Args {
   int32_t* err;
   Plan* plan;        // workspace: [B]
   Pair* pair;        // [B][Hkv]
-  float2* part_ml;   // [G][slots] running max (log2 units) and sum
+  float2* part_ml;   // [G][slots] reference of the scores (log2 units) and sum
   float* part_o;     // [slot][d/128][G][128]
   float2* half_w;    // [B][bt_stride][2][H] half pages' sums and the max they refer to (-inf: unseen)
   long long n_pages;
@@ -322,11 +326,12 @@ struct Misc {
   Rec rec[MAXREC];
   int plane[YRING];                // K planes of the pages looked up, -1: outside the pool
   float red[4][HP];
-  __align__(16) float m[HP];       // running max per head (log2 units), 0 while nothing was seen
+  __align__(16) float m[HP];       // what a head's scores are taken relative to (log2 units): its
+                                   //   running max, less the lift in fp16; 0 while nothing was seen
   __align__(16) float over[HP];    // running max + RESCALE_LOG2, -inf while nothing was seen
   __align__(16) float alpha[HP];
   __align__(16) float slope[HP];   // slope * log2 e
-  float m_raw[HP];                 // running max, -inf while nothing was seen
+  float m_raw[HP];                 // the same reference, -inf while nothing was seen
 };
 
 // Exclusive prefixes over the CTA's threads of a cost and of a flag; tot receives the sums.
@@ -846,6 +851,7 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
       const bool f16 = a.f16 != 0;
       const float scale2 = a.cap > 0.f ? a.scale / a.cap : a.scale * LOG2E;
       const float cap2 = a.cap * LOG2E;
+      const float lift = f16 ? LIFT_F16_LOG2 : 0.f;
       constexpr int HL = HW >= 32 ? HW / 32 : 1;  // heads whose sums a lane holds, from h_lane on
       const int h_lane = hb + (HW >= 32 ? lane * HL : lane >> 1);
       bool failed = false;
@@ -961,10 +967,13 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
                 const float old = m->m_raw[h];
                 float al = 1.f;
                 if (top > m->over[h]) {    // an unset max takes any score: the sums so far are 0
-                  al = exp2f(old - top);
-                  m->m_raw[h] = top;
-                  m->m[h] = top;
-                  m->over[h] = top + RESCALE_LOG2;
+                  // rounded so that no score up to `over` gets more than 2^(lift + 8), however
+                  // far apart fp32 numbers of this size are
+                  const float ref = __fadd_ru(top, -lift);
+                  al = exp2f(old - ref);
+                  m->m_raw[h] = ref;
+                  m->m[h] = ref;
+                  m->over[h] = __fadd_rd(ref, lift + RESCALE_LOG2);
                 }
                 m->alpha[h] = al;
               }
@@ -982,8 +991,9 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
               x[h + 2] = ex2_approx(x[h + 2] - mm.z);
               x[h + 3] = ex2_approx(x[h + 3] - mm.w);
             }
-            // P is rounded to the operands' type, which the product needs (at most half an ulp of
-            // each weight); the sums take the weights as they were before
+            // P is rounded to the operands' type, which the product needs: at most half an ulp of
+            // each weight, in fp16 at least 2^-25, which is 2^-32 of the row's largest weight. The
+            // sums take the weights as they were before
             if (f16) {
 #pragma unroll
               for (int h = 0; h < HW; h += 2) pw[h / 2] = pack16(x[h], x[h + 1], true);

@@ -196,3 +196,80 @@ def test_scores_of_minus_infinity_only_give_zeros(cuda_ok, lens):
     want = c.score0.clone()
     want[0, :int(c.n[0])] *= c.decay
     assert torch.equal(c.tables.score.cpu(), want)
+
+
+# ------------------------------------------------------------- weights far below the largest one
+def peaked(c, b, nats):
+    """Sequence b's newest token outweighs every other by `nats` in every head; it has the value 0, so
+    that the output is what the others' small weights make of it."""
+    n, t = int(c.n[b]), int(c.tail[b])
+    page = int(c.table[b, n - 1])
+    c.cache.pool[page, 0, :, t - 1] = 0
+    c.cache.pool[page, 0, :, t - 1, 0] = 16.0
+    c.cache.pool[page, 1, :, t - 1] = 0
+    c.q[b, :, 0] = nats / (16.0 * c.scale)
+
+
+FLAT = [
+    # lens, H, Hkv, d, nats: all but the newest token of the same key, weights at and below 2^-24
+    ([128], 4, 1, 128, 17.4), ([100, 7], 16, 2, 128, 17.0), ([64], 64, 1, 512, 18.0), ([128], 24, 1, 256, 16.0),
+    ([9000, 2000], 8, 2, 128, 17.4), ([4097], 64, 1, 512, 17.4),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("lens,H,Hkv,d,nats", FLAT, ids=lambda x: str(x).replace(" ", ""))
+def test_small_weights_count(cuda_ok, lens, H, Hkv, d, nats, dtype):
+    c = Case(lens, H, Hkv, d, dtype, seed=31, junk=False)
+    for b in range(c.B):
+        own = torch.from_numpy(c.table[b, :int(c.n[b])].astype(np.int64)).to(DEV)
+        c.cache.pool[own, 0] = 0
+        c.cache.pool[own, 1] = c.cache.pool[own, 1].abs() * 256 + 256       # outputs in fp16's normal range
+        peaked(c, b, nats)
+    check(c.run())
+
+
+@pytest.mark.parametrize("nats", [12.0, 14.0, 16.0])
+def test_small_weights_of_whole_pairs_count(cuda_ok, nats):
+    """592 pairs over 296 CTAs: a row of 8,192 tokens, scores N(0, 1) but for the newest token's, in
+    one segment. The tables name the same pages many times."""
+    B, Hkv, d, E = 74, 8, 128, 128
+    c = Case([64 * E] + [64] * 199, Hkv, Hkv, d, "fp16", seed=32, junk=False, score=False)
+    g = np.random.default_rng(5)
+    table = g.choice(c.table[0, :E], (B, E)).astype(np.int32)
+    table[:, -1] = c.table[1:B + 1, 0]
+    c.B, c.E, c.table, c.pos = B, E, table, np.tile(np.arange(E), (B, 1))
+    c.lens, c.n, c.tail = np.full(B, 64 * E), np.full(B, E), np.full(B, 64)
+    c.prefix = c.docs = np.zeros(B, np.int64)
+    c.q = c.q[:B].clone()
+    c.cache.pool[:, 1] = c.cache.pool[:, 1] * 0.5 + 1
+    c.cache.pool[:, 0, :, :, 0] = 0
+    old = c.cache
+    c.tables = lsa.LsaPagedTables(i32(table), i32(c.n), i32(c.tail), i32(c.pos))
+    c.cache = lsa.LsaPagedCache(old.pool, c.tables, c.H)
+    c.out = torch.empty((B, c.H, d), dtype=c.t, device=DEV)
+    for b in range(B):
+        peaked(c, b, nats)
+    check(c.run(), seqs=[0, 1, 36, 73])
+    # and with values of mean 1 under the newest token too
+    c.cache.pool[torch.from_numpy(table[:, -1].astype(np.int64)).to(DEV), 1, :, -1] = 1
+    check(c.run(), seqs=[0, 40, 73])
+
+
+def test_scores_too_large_for_the_weights_scale(cuda_ok):
+    """Score differences of 2^20 and more, where neighbouring fp32 numbers are further apart than the
+    room above the running max: one token takes all the weight, and none overflows."""
+    c = Case([1000, 70], 8, 2, 128, "fp16", seed=33, q_scale=1.0, junk=False)
+    for k in (4096.0, 32768.0):                  # powers of two: equal sums stay equal in fp32
+        c.q = (torch.sign(c.q.float()) * k).to(c.t)
+        c.cache.pool[:, 0] = torch.sign(c.cache.pool[:, 0]) * k
+        big = (c.q.float().abs().max() * c.cache.pool[:, 0].float().abs().max()).item()
+        assert big > 2 ** 23
+        c.tables.score.copy_(c.score0)
+        c.run()
+        assert c.cache.read_err() == 0 and torch.isfinite(c.out.float()).all()
+        for b in range(c.B):
+            # the weights are 1 / m for the m largest scores: sums of +-1, equal ones exactly so
+            ref = reference(c, b)[0]
+            got = c.out[b].double().cpu().numpy()
+            assert (np.abs(got - ref) <= 2.0 ** -9 * np.abs(c.pool.float().abs().max().item())).all()
