@@ -273,3 +273,20 @@ def test_scores_too_large_for_the_weights_scale(cuda_ok):
             ref = reference(c, b)[0]
             got = c.out[b].double().cpu().numpy()
             assert (np.abs(got - ref) <= 2.0 ** -9 * np.abs(c.pool.float().abs().max().item())).all()
+
+
+# ---------------------------------------------------------------------------- long rows
+LONG = [
+    ([1000 + 37 * i for i in range(16)], 32, 8, 128, dict(cap=30.0, window=700, prefix=[100 + i for i in range(16)])),
+    ([20017], 64, 1, 512, dict(window=15001, prefix=[700], gap=2)),
+    ([8003, 16001], 32, 2, 384, dict(prefix=[1000, 33], docs=[4001, 9000])),
+    ([50021], 64, 2, 128, dict(prefix=[5000], window=40000)),
+    ([30011], 20, 1, 512, dict(window=20000)),
+    ([100003], 4, 1, 128, {}),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("lens,H,Hkv,d,kw", LONG, ids=[str(c[0][0]) for c in LONG])
+def test_long_rows_by_their_norm(cuda_ok, lens, H, Hkv, d, kw, dtype):
+    check(Case(lens, H, Hkv, d, dtype, seed=H, **kw).run(), seqs=range(0, len(lens), 5), norm=True)
