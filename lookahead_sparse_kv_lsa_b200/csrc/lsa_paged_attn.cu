@@ -5,8 +5,9 @@
 //   z = scale q.K(x), capped: c tanh(z / c), minus slope_h (x_b - x);  w = softmax(z);
 //   out = sum w V(x);  score[page of x] += w.
 // All softmax arithmetic is in log2 units (z * log2 e), in fp32. The bias is taken relative
-// to the last seen position instead of x_b: a constant per head, which the softmax drops,
-// and the differences that matter stay small numbers however long the cache is.
+// to the last seen position instead of x_b, or to the first seen block where the slope is
+// negative: a constant per head, which the softmax drops. The tokens that the bias favours then
+// have a small one, which fp32 holds with the score's own precision however long the cache is.
 //
 // What bounds it: every key and value is read once, 4 d Hkv bytes a token against
 // 4 H d flops, so H / Hkv flop per byte; on a B200 that is HBM bandwidth for any group of
@@ -74,7 +75,8 @@ constexpr int LANE_PARTS = MAX_CTAS / 32;   // parts per lane, at most
 
 // One sequence, as an attention CTA sees it.
 struct Rec {
-  long long ref;     // last position of its last seen entry (origin of the bias)
+  long long ref;     // last position of its last seen entry: origin of a bias that falls with distance
+  long long ref_low; // first position of its first seen entry: origin of a bias that rises
   long long low;     // positions >= low are seen,
   int pre;           //   and those < pre
   int b, pages;      // seen entries; 0: nothing seen
@@ -191,6 +193,7 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
   r.b = b;
   r.base = 0;
   r.ref = 0;
+  r.ref_low = 0;
   r.low = 0;
   r.pre = 0;
   r.pages = r.n = r.tail = r.e1 = r.e2 = r.masked = 0;
@@ -235,8 +238,12 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
         if (tail < PAGE) r.dirty = r.e1;
       }
     }
-    const int j = r.e2 < n ? n - 1 : r.e1 - 1;                // last seen entry
-    r.ref = (j == n - 1 || !pos ? (pos ? last : j) : pos[j < 0 ? 0 : j]) * static_cast<long long>(PAGE) + PAGE - 1;
+    if (a.slopes != nullptr) {
+      const int j = r.e2 < n ? n - 1 : r.e1 - 1;              // last seen entry
+      r.ref = (j == n - 1 || !pos ? (pos ? last : j) : pos[j < 0 ? 0 : j]) * static_cast<long long>(PAGE) + PAGE - 1;
+      const int i = r.e1 > 0 ? 0 : r.e2;                      // first seen entry
+      r.ref_low = (i == 0 || !pos ? (pos ? first : i) : pos[i < n ? i : n - 1]) * static_cast<long long>(PAGE);
+    }
   }
   r.pages = r.e1 + n - r.e2;
   return r;
@@ -922,14 +929,14 @@ __global__ void __launch_bounds__(Roles<HP>::NT, (Layout<HP, NDC>::CTAS_PER_SM))
                 for (int h = 0; h < HW; ++h) x[h] *= scale2;
               }
               if (a.slopes != nullptr) {
-                const float rel = static_cast<float>(x0 - r.ref);
+                const float fall = static_cast<float>(x0 - r.ref), rise = static_cast<float>(x0 - r.ref_low);
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
                   const float4 s = *reinterpret_cast<const float4*>(m->slope + hb + h);
-                  x[h] = fmaf(s.x, rel, x[h]);
-                  x[h + 1] = fmaf(s.y, rel, x[h + 1]);
-                  x[h + 2] = fmaf(s.z, rel, x[h + 2]);
-                  x[h + 3] = fmaf(s.w, rel, x[h + 3]);
+                  x[h] = fmaf(s.x, s.x < 0.f ? rise : fall, x[h]);
+                  x[h + 1] = fmaf(s.y, s.y < 0.f ? rise : fall, x[h + 1]);
+                  x[h + 2] = fmaf(s.z, s.z < 0.f ? rise : fall, x[h + 2]);
+                  x[h + 3] = fmaf(s.w, s.w < 0.f ? rise : fall, x[h + 3]);
                 }
               }
               if (sees != 0xffffffffu) {

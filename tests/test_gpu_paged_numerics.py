@@ -290,3 +290,19 @@ LONG = [
 @pytest.mark.parametrize("lens,H,Hkv,d,kw", LONG, ids=[str(c[0][0]) for c in LONG])
 def test_long_rows_by_their_norm(cuda_ok, lens, H, Hkv, d, kw, dtype):
     check(Case(lens, H, Hkv, d, dtype, seed=H, **kw).run(), seqs=range(0, len(lens), 5), norm=True)
+
+
+# --------------------------------------------------------------------- biases of either sign
+@pytest.mark.parametrize("lens,H,Hkv,d,kw", [
+    ([100003], 4, 1, 128, {}),
+    ([30000], 8, 2, 128, dict(gap=40)),                         # over 1.2M positions
+    ([30000, 2000], 8, 2, 128, dict(gap=40, prefix=[300, 0], window=200000)),
+    ([9000, 500], 8, 2, 128, dict(gap=40, docs=[100000, 999], cap=20.0)),
+    ([9000], 40, 1, 256, dict(gap=100)),
+    ([5000, 30, 0], 64, 1, 512, dict(gap=200)),
+    ([50, 64, 65, 1], 8, 8, 128, {}),
+], ids=lambda x: str(x)[:24].replace(" ", ""))
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_biases_of_either_sign_over_long_distances(cuda_ok, lens, H, Hkv, d, kw, dtype):
+    slopes = np.resize([-0.5, 0.5, -2.0, 0.0, -0.01, 1.0, -1e-4, 1e-6], H)
+    check(Case(lens, H, Hkv, d, dtype, seed=41, slopes=slopes, **kw).run())
