@@ -215,7 +215,9 @@ __device__ __forceinline__ Rec read_seq(const Args& a, int b, bool& bad) {
       r.masked = 1;
       r.low = low;
       r.pre = pre < 0 ? 0 : pre;
-      r.e2 = first_at_least(pos, n, first, last, low >> 6);   // its last position >= low
+      // the first entry whose last position is >= low; none where a document starts behind the
+      // newest token, be it in the tail block's unfilled slots
+      r.e2 = low > last * PAGE + tail - 1 ? n : first_at_least(pos, n, first, last, low >> 6);
       if (r.pre > 0) r.e1 = first_at_least(pos, n, first, last, (static_cast<long long>(r.pre) + PAGE - 1) >> 6);
       const bool hole = r.e1 > r.e2;                          // one entry holds both bounds
       if (hole) r.e1 = r.e2;

@@ -306,3 +306,31 @@ def test_long_rows_by_their_norm(cuda_ok, lens, H, Hkv, d, kw, dtype):
 def test_biases_of_either_sign_over_long_distances(cuda_ok, lens, H, Hkv, d, kw, dtype):
     slopes = np.resize([-0.5, 0.5, -2.0, 0.0, -0.01, 1.0, -1e-4, 1e-6], H)
     check(Case(lens, H, Hkv, d, dtype, seed=41, slopes=slopes, **kw).run())
+
+
+# ------------------------------------------------------------------------- blocks nobody sees
+@pytest.mark.parametrize("prefix", [None, [100, 0, 64, 576]])
+@pytest.mark.parametrize("gap", [1, 3])
+def test_a_document_that_starts_behind_the_newest_token(cuda_ok, prefix, gap):
+    """doc_start in the tail block's unfilled slots: no slot of that block is seen, and it is not
+    looked at. Its table entry lies outside the pool."""
+    c = Case([600, 577, 10, 639], 8, 2, 128, seed=51, gap=gap, docs=[0] * 4, prefix=prefix)
+    n = c.n - 1
+    c.docs = 64 * c.pos[np.arange(4), n] + c.tail + np.array([0, 5, 3, 0])
+    c.cache.doc_start.copy_(i32(c.docs))
+    if prefix is not None:                       # up to the tail block, not into it
+        c.prefix = np.minimum(c.prefix, 64 * c.pos[np.arange(4), n])
+        c.cache.prefix_len.copy_(i32(c.prefix))
+    c.table[np.arange(4), n] = [-1, 1 << 20, -7, c.pages]
+    c.tables.block_table.copy_(i32(c.table))
+    check(c.run())
+
+
+def test_a_prefix_that_reaches_into_an_unseen_tail_block(cuda_ok):
+    c = Case([600, 577, 10, 640], 8, 2, 128, seed=52, docs=[610, 578, 11, 10 ** 6], prefix=[590, 577, 64, 600],
+             junk=True)
+    check(c.run())
+    c.table[0, -1] = -1                          # the prefix reaches this one
+    c.tables.block_table.copy_(i32(c.table))
+    c.tables.score.copy_(c.score0)
+    check(c.run(), err=_lib.DEVERR_BAD_PAGE)
