@@ -428,7 +428,10 @@ lsa_status lsa_denoise_labels(const float* logits, int32_t n_windows, int32_t n_
  * page carries a running score, the attention weight it received, and the pages with the
  * smallest scores are given back when a sequence holds more than its budget. With
  * Hkv = 1 the pool is the pool of lsa_decode_attn, and a block table of lsa_gather can be
- * attended with the options below.
+ * attended. lsa_gather writes no positions: a window, a bias, prefix_len or doc_start on such
+ * a table needs a block_pos of the caller's, the ids of the kept blocks and then of the
+ * window's: block_pos[b][j] = sel_ids[b][j] for j < sel_cnt[b], block_pos[b][sel_cnt[b] + i] =
+ * n_cand[b] + i. A cap and page weights need none.
  *
  * Sequence b holds the entries j < n_entries[b] of its table row. Entry j is page
  * block_table[b][j] of the pool and block block_pos[b][j] of the sequence: slot t of it is
@@ -446,7 +449,8 @@ lsa_status lsa_denoise_labels(const float* logits, int32_t n_windows, int32_t n_
 typedef struct lsa_paged_tables {
   int32_t* block_table;  /* device i32 [B][bt_stride] */
   int32_t* block_pos;    /* device i32 [B][bt_stride], strictly ascending within a sequence's
-                            entries, each in [0, 2^25); NULL: entry j is block j */
+                            entries, each in [0, 2^25); NULL: entry j is block j, which is wrong
+                            for a table with blocks left out */
   float* score;          /* device f32 [B][bt_stride]; NULL: no scores are kept */
   int32_t* n_entries;    /* device i32 [B], 0 .. bt_stride */
   int32_t* tail_len;     /* device i32 [B], 1 .. 64 (not read where n_entries is 0) */

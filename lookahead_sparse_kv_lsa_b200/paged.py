@@ -38,8 +38,9 @@ def _check(t, dtype, name: str, shape, device) -> Optional[int]:
 
 class LsaPagedTables:
     """The page tables of a batch (lsa_paged_tables): block_table i32 [B][E], block_pos i32
-    [B][E] or None (entry j is block j), score f32 [B][E] or None, n_entries and tail_len i32
-    [B], free_list i32 [B][F] and free_cnt i32 [B], or None (no pages to take or give back)."""
+    [B][E] or None (entry j is block j: not for tables with blocks left out, as lsa_gather's),
+    score f32 [B][E] or None, n_entries and tail_len i32 [B], free_list i32 [B][F] and free_cnt
+    i32 [B], or None (no pages to take or give back)."""
 
     def __init__(self, block_table, n_entries, tail_len, block_pos=None, score=None,
                  free_list=None, free_cnt=None):

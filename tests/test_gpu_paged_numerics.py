@@ -334,3 +334,51 @@ def test_a_prefix_that_reaches_into_an_unseen_tail_block(cuda_ok):
     c.tables.block_table.copy_(i32(c.table))
     c.tables.score.copy_(c.score0)
     check(c.run(), err=_lib.DEVERR_BAD_PAGE)
+
+
+# ------------------------------------------------------------------ tables of the LSA step driver
+def test_options_on_a_gathered_table(cuda_ok):
+    """lsa_gather writes no positions. Formed as the header says, from the ids of the kept blocks and
+    of the window's, they give window, document, prefix and bias their meaning on its table."""
+    from types import SimpleNamespace
+
+    import lsa_inputs as LI
+    wl = LI.Workload(LI.tiny(), pin=True)
+    cfg, dev = wl.cfg, torch.device("cuda")
+    nc = max(1, max((int(x) - cfg.W) // 64 for x in wl.ctx0))
+    dec = lsa.LsaDecoder(wl.w_q.to(dev), wl.k_idx.to(dev), wl.blk_off[:cfg.B], torch.from_numpy(wl.bias).to(dev),
+                         wl.host_pool, wl.blk_off, wl.nb0, W=cfg.W, H=cfg.H, cap=nc, max_cand=nc, scale=cfg.scale)
+    dec.load_window(0)
+    k, v = wl.kv_new(0, 0)
+    a = torch.empty((cfg.B, cfg.H, cfg.d), dtype=torch.bfloat16, device=dev)
+    dec.step(0, wl.h(0).to(dev), wl.q(0, 0).to(dev), k.to(dev), v.to(dev), a)
+    torch.cuda.synchronize()
+    assert dec.read_err() == 0
+    E = dec.block_table.shape[1]
+    j = torch.arange(E, dtype=torch.int32, device=dev)[None]
+    kept = dec.sel_cnt[:, None]
+    ids = torch.cat([dec.sel_ids, torch.zeros((cfg.B, E - dec.sel_ids.shape[1]), dtype=torch.int32, device=dev)], 1)
+    pos = torch.where(j < kept, ids, dec.n_cand[:, None] + j - kept)
+    n = dec.n_entries.cpu().numpy()
+    assert any((np.diff(pos[b, :n[b]].cpu().numpy()) > 1).any() for b in range(cfg.B))      # blocks were left out
+    assert [int(pos[b, n[b] - 1]) for b in range(cfg.B)] == [int(x) for x in wl.nb0]
+    W = int(cfg.W)
+    for kw in (dict(slopes=True), dict(window=2 * W + 700), dict(docs=True), dict(window=W // 2, prefix=True, cap=5.0, slopes=True)):
+        c = SimpleNamespace(B=cfg.B, H=cfg.H, Hkv=1, d=cfg.d, E=E, t=torch.bfloat16, dtype="bf16", cap=kw.get("cap", 0.0),
+                            window=kw.get("window", 0), decay=0.5, scale=float(np.float32(cfg.scale)), n=n,
+                            tail=dec.tail_len.cpu().numpy(), table=dec.block_table.cpu().numpy(), pos=pos.cpu().numpy(),
+                            q=wl.q(0, 0), pages=dec.n_pages, score0=torch.rand((cfg.B, E)), slopes=None)
+        last = 64 * np.asarray(wl.nb0)
+        c.prefix = np.full(cfg.B, 1000 if "prefix" in kw else 0)
+        c.docs = last // 3 + 17 if "docs" in kw else np.zeros(cfg.B, np.int64)
+        if "slopes" in kw:
+            c.slopes = (2.0 ** -np.arange(6, 6 + cfg.H)).astype(np.float32)
+        c.tables = lsa.LsaPagedTables(dec.block_table, dec.n_entries, dec.tail_len, pos.contiguous(), c.score0.to(dev))
+        c.cache = lsa.LsaPagedCache(dec.hbm_pool.unsqueeze(2), c.tables, cfg.H, scale=cfg.scale, cap=c.cap, window=c.window,
+                                    decay=0.5, slopes=None if c.slopes is None else torch.from_numpy(c.slopes).to(dev),
+                                    prefix_len=i32(c.prefix) if "prefix" in kw else None,
+                                    doc_start=i32(c.docs) if "docs" in kw else None)
+        c.out = torch.empty_like(a)
+        c.cache.attend(c.q.to(dev), c.out)
+        torch.cuda.synchronize()
+        check(c)
