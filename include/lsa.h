@@ -463,7 +463,9 @@ typedef struct lsa_paged_cache {
   int32_t H, Hkv;        /* query heads and key heads; H / Hkv query heads share a key head */
   int32_t d;             /* head dimension: 128, 256, 384 or 512 */
   int32_t dtype;         /* LSA_DTYPE_*: type of the pool, of q, k_new, v_new and out */
-  int32_t bt_stride, free_stride;  /* B * Hkv * (bt_stride + 16) <= 2^30 */
+  int32_t bt_stride, free_stride;  /* B * Hkv * (bt_stride + 16) <= 2^30. The attention's workspace
+                            and launches, and the eviction kernel, go by bt_stride, not by n_entries:
+                            tables no wider than their use are faster */
   int32_t window;        /* > 0: sliding window in tokens, the newest one included; 0: none */
   float scale;           /* attention scale, > 0 */
   float cap;             /* > 0: scores are cap * tanh(scale * q.k / cap); 0: no cap */

@@ -12,12 +12,13 @@
 // What bounds it: every key and value is read once, 4 d Hkv bytes a token against
 // 4 H d flops, so H / Hkv flop per byte; on a B200 that is HBM bandwidth for any group of
 // up to 64 heads, as long as the products run on the tensor cores. Measured (profiler: the DRAM
-// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512, 352 us for 2.15 GB, 93 % of
-// the copy bandwidth, or 365 to 390 us where the power cap holds the SMs at 1.6 to 1.7 GHz (a tile
-// takes a CTA some 10,400 cycles); a ragged batch of 64 with 8 key heads of 128, 52.5 us for 261
-// MB, 76 %; some 1,350 kept pages of the 1M tokens, 48.9 us for 177 MB, 55 %. Below some 500 MB the
-// fixed costs count: planning and the first tile (about 4 us), the last product and the epilogue
-// (3 to 4 us), the joining kernel (1 us to start, 3 to 5 us), and segments that end unevenly.
+// bytes read are the algorithmic ones): 1M tokens of 64 heads of 512 with page weights, 360 us for
+// 2.15 GB in short runs, 91 % of the copy bandwidth, and 364 to 391 us where the power cap holds the
+// SMs at 1.6 to 1.7 GHz (a tile takes a CTA some 10,400 cycles); a ragged batch of 64 with 8 key
+// heads of 128, 53.8 us for 261 MB, 74 %; some 1,350 kept pages of the 1M tokens, 49.4 us for 177
+// MB, 55 %. Below some 500 MB the fixed costs count: planning and the first tile (about 4 us), the
+// last product and the epilogue (3 to 4 us), the joining kernel (1 us to start, 3 to 5 us), and
+// segments that end unevenly.
 //
 // Work split. The seen pages of a sequence are its first e1 entries (prefix) and those from
 // e2 on (document, window), the same for each key head. Every pair (sequence, key head) with
@@ -36,7 +37,9 @@
 //             tokens), accumulated in TMEM;
 //   warps 2-.. softmax, a token row (of up to 32 heads: 64 heads take two groups of four
 //             warps) per thread: the row's scores stay in registers from the
-//             one TMEM load to the rounding of P. A vote (one barrier with reduction) finds
+//             one TMEM load to the rounding of P (at 168 registers a thread the kernels for 64
+//             heads spill 740 to 910 bytes and load 170 to 260 back, those for 32 heads 300 to
+//             730 and 100 to 160, those for 16 heads next to nothing). A vote (one barrier with reduction) finds
 //             whether any score exceeds its head's running max by more than 2^8; only then is
 //             the tile max formed and O^T rescaled. Each half page's per-head sums (a butterfly
 //             over the warp's 32 rows) feed the denominators and, where scores are kept, go
@@ -1503,6 +1506,9 @@ lsa_status launch(const CUtensorMap& mkv, const CUtensorMap& mq, Args a, int n_s
   // A block for each 128 dims of a head where pairs are split over 24 CTAs or more on average, else
   // a warp: one sequence of 16K or 1M tokens takes 11.7 or 48.9 us with blocks, 19.1 or 64.9 us with
   // warps; 8 of 128K or 64 ragged ones take 60.5 or 63.1 us with blocks, 52.9 or 52.5 us with warps.
+  // 64 heads of 512 at 49, 30, 25 and 21 CTAs a pair: 46.0, 48.2, 49.3 and 50.4 us with blocks, 49.8,
+  // 46.3, 45.6 and 44.7 us with warps; 8 heads of 128 at 37, 25 and 23: 23.9, 24.3 and 25.0 us against
+  // 24.1, 23.9 and 24.3 us. The two sides meet near 37; between 24 and 37 up to 4 us are given away.
   ja.wide = static_cast<long long>(a.B) * a.Hkv * 24 <= ctas;
   ja.per_head = 1;
   while (ja.per_head < 32 && 2 * ja.per_head * a.H <= lsa::paged::JOIN_THREADS) ja.per_head *= 2;
